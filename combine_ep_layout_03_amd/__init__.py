@@ -1,6 +1,7 @@
 """MoE token dispatch / combine for one MI355X (gfx950).
 
-A thin binding over the C ABI in include/ep_mi355x.h: each function checks
+A thin binding over the C ABI in include/ep_mi355x.h (here) and
+include/ep_mi355x_layer.h (layer.py): each function checks
 that the torch tensors it is handed are contiguous device tensors of the
 right dtype and shape, allocates outputs with torch (device memory is the
 only thing torch provides here), and calls the library entry point of the
@@ -33,6 +34,8 @@ from ._lib import (  # noqa: F401
     EP_STATUS_ROWS_EXPERT,
     EP_STATUS_ROWS_GROUP,
     EP_STATUS_WORDS,
+    EP_SCORE_SIGMOID,
+    EP_SCORE_SOFTMAX,
     EPError,
 )
 
@@ -52,6 +55,12 @@ __all__ = [
     "PackedExpertWeights",
     "ep_expert_weights_packed_bytes",
     "ep_pack_expert_weights",
+    "ep_route",
+    "ep_route_backward",
+    "ep_combine_backward",
+    "ep_lora_workspace_bytes",
+    "ep_lora",
+    "ep_lora_backward",
     "ep_strerror",
     "EPError",
 ]
@@ -599,3 +608,13 @@ def ep_expert_gemm(
     )
     _lib.check("ep_expert_gemm", rc)
     return out
+
+
+from .layer import (  # noqa: E402  (built on the helpers above)
+    ep_combine_backward,
+    ep_lora,
+    ep_lora_backward,
+    ep_lora_workspace_bytes,
+    ep_route,
+    ep_route_backward,
+)

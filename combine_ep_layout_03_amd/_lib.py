@@ -1,4 +1,5 @@
-"""ctypes loader for the HIP library and the C structs of include/ep_mi355x.h.
+"""ctypes loader for the HIP library and the C structs of include/ep_mi355x.h
+and include/ep_mi355x_layer.h.
 
 There is no fallback: if the library is not built, loading raises.
 """
@@ -46,6 +47,14 @@ EP_ROWS_GROUP = 1
 EP_COMBINE_FLAT = 0
 EP_COMBINE_GROUPED = 1
 
+EP_MAX_ROUTE_GROUPS = 64
+EP_MAX_LORA_RANK = 128
+EP_SCORE_SOFTMAX = 0
+EP_SCORE_SIGMOID = 1
+EP_LOGITS_FP32 = 0
+EP_LOGITS_BF16 = 1
+EP_LORA_SCATTER_ROWS = 1
+
 EXPORTS = (
     "ep_fp8_row_bytes",
     "ep_layout_workspace_bytes",
@@ -57,6 +66,12 @@ EXPORTS = (
     "ep_expert_weights_packed_bytes",
     "ep_pack_expert_weights",
     "ep_strerror",
+    "ep_route",
+    "ep_route_backward",
+    "ep_combine_backward",
+    "ep_lora_workspace_bytes",
+    "ep_lora",
+    "ep_lora_backward",
 )
 
 
@@ -89,6 +104,32 @@ class LayoutStruct(ctypes.Structure):
         ("expert_row_capacity", ctypes.c_int64),
         ("recv_stats", ctypes.c_void_p),
         ("generation", ctypes.c_uint32),
+    ]
+
+
+class Router(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("num_experts", ctypes.c_int32),
+        ("topk", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("logits", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class LoraWeights(ctypes.Structure):
+    _fields_ = [
+        ("a", ctypes.c_void_p),
+        ("b", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("rank", ctypes.c_int32),
+        ("n_out", ctypes.c_int32),
+        ("flags", ctypes.c_int32),
     ]
 
 
@@ -133,6 +174,21 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     L.ep_expert_weights_packed_bytes.restype = ctypes.c_int64
     L.ep_pack_expert_weights.argtypes = [vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vp, vp]
     L.ep_pack_expert_weights.restype = ctypes.c_int
+    RT = ctypes.POINTER(Router)
+    LW = ctypes.POINTER(LoraWeights)
+    i64 = ctypes.c_int64
+    L.ep_route.argtypes = [RT, vp, vp, vp, vp, vp, vp]
+    L.ep_route.restype = ctypes.c_int
+    L.ep_route_backward.argtypes = [RT, vp, vp, vp, vp, vp]
+    L.ep_route_backward.restype = ctypes.c_int
+    L.ep_combine_backward.argtypes = [P, LS, vp, vp, vp, i64, vp, vp, vp]
+    L.ep_combine_backward.restype = ctypes.c_int
+    L.ep_lora_workspace_bytes.argtypes = [P, LW, ctypes.c_int32]
+    L.ep_lora_workspace_bytes.restype = ctypes.c_size_t
+    L.ep_lora.argtypes = [P, LS, LW, vp, i64, vp, i64, vp, i64, vp, ctypes.c_size_t, vp]
+    L.ep_lora.restype = ctypes.c_int
+    L.ep_lora_backward.argtypes = [P, LS, LW, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, ctypes.c_size_t, vp]
+    L.ep_lora_backward.restype = ctypes.c_int
     L.ep_strerror.argtypes = [ctypes.c_int]
     L.ep_strerror.restype = ctypes.c_char_p
     if path is None:
