@@ -1,17 +1,23 @@
 // Router: each token's K experts of largest selection value, and its weights.
 //
-// LPT lanes work on one token (16 up to 256 experts, 32 up to 512, 64 up to
-// 1024), so a wave takes 64 / LPT tokens and the reductions of K rounds run
-// for all of them at once; lane g of a token holds experts j * 4 * LPT + 4 g
-// + c (c < 4), up to NV of them in registers.
+// LPT lanes work on one token; lane g holds experts j * 4 * LPT + 4 g + c (c <
+// 4), NV of them in registers.  With 16 lanes a wave takes four tokens and
+// each step of a reduction runs for all four; with 64 a token has the
+// shortest chain of steps (see route_e for the choice).
 //
-// The K rounds find a maximum over keys (value, then lowest index, in one
-// unsigned integer: 64 bits, or 32 for bf16 logits without a bias) and drop
-// it.  Values that a rounding could order wrongly (scores plus a bias, sums
-// of scores) are computed in fp32 with a bound on their error; a token whose
-// neighbouring values lie within it, and are not the values of one and the
-// same logit and bias, is done again in binary64.  That is about one token in
-// a thousand, and gives the order of the binary64 values for all.
+// A key is one 32-bit integer: the value in an order-preserving form, its low
+// bits replaced by the complement of the expert's place among the lane's (of
+// equal keys in two lanes the lower lane's goes first).  Each lane sorts its
+// keys once; a round then is a maximum over the lanes' heads and a shift in
+// the lane that held it.  For bf16 logits without a bias the low 16 bits are
+// free for the whole index and nothing is lost.  Otherwise the rounds order the experts only up to a tolerance (the bits
+// given up, and the error of scores computed with the hardware's exponential
+// and reciprocal), so neighbours closer than it are put in order by their exact
+// values: the fp32 logits, or score + bias in binary64.  That takes one
+// binary64 score per candidate, for the candidates down to the first clear gap
+// below the Kth.  Groups are treated alike.  Where even that leaves doubt (too
+// many candidates, a group whose best two are in doubt) the token is done
+// again in binary64 throughout.
 #include <float.h>
 
 #include "ep_layer.h"
@@ -45,6 +51,19 @@ __device__ __forceinline__ float clean_logit(float l) {
   return l != l ? kNegInf : fminf(l, FLT_MAX) + 0.0f;
 }
 
+// A chosen expert's score up to a factor common to its token's chosen ones,
+// whose largest logit is top: exp(l - top), or sigmoid(l) / exp(min(top, 0)),
+// neither of which underflows for the largest.
+__device__ __forceinline__ float relative_score(float l, float top, bool sigmoid) {
+  if (!sigmoid) return expf(l - top);
+  return l < 0.0f ? expf(l - fminf(top, 0.0f)) / (1.0f + expf(l)) : 1.0f / (1.0f + expf(-l));
+}
+
+__device__ __forceinline__ float sigmoid32(float l) {
+  const float e = expf(-fabsf(l));  // at most 1, so nothing overflows and small scores stay
+  return (l < 0.0f ? e : 1.0f) / (1.0f + e);
+}
+
 // order-preserving map to unsigned integers
 __device__ __forceinline__ uint32_t ordered(float f) {
   const uint32_t b = __float_as_uint(f);
@@ -52,6 +71,10 @@ __device__ __forceinline__ uint32_t ordered(float f) {
 }
 __device__ __forceinline__ float unordered(uint32_t o) {
   return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+
+__device__ __forceinline__ int64_t wave_task() {
+  return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
 }
 
 // ------------------------------------------------- reductions over LPT lanes
@@ -92,21 +115,52 @@ struct Min {
     return a < b ? a : b;
   }
 };
+struct Or {
+  __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a | b; }
+};
 struct Sum {
   template <typename T>
   __device__ __forceinline__ T operator()(T a, T b) const {
     return a + b;
   }
 };
-// the reduction of v over the token's LPT lanes, in every one of them
+// f of v and the v of the other row of 16 (or half of 32): the swap leaves
+// the even rows' values in one result and the odd rows' in the other
+template <int N, typename F>
+__device__ __forceinline__ uint32_t across(uint32_t v, F f) {
+  if constexpr (N == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return f(static_cast<uint32_t>(r[0]), static_cast<uint32_t>(r[1]));
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return f(static_cast<uint32_t>(r[0]), static_cast<uint32_t>(r[1]));
+  }
+}
+template <int N, typename F>
+__device__ __forceinline__ float across(float v, F f) {
+  return __uint_as_float(across<N>(__float_as_uint(v), [&](uint32_t a, uint32_t b) {
+    return __float_as_uint(f(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+template <int N, typename F>
+__device__ __forceinline__ double across(double v, F f) {
+  return f(v, turn<N>(v));
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v)));
+}
+__device__ __forceinline__ float uniform(float v) { return __uint_as_float(uniform(__float_as_uint(v))); }
+__device__ __forceinline__ double uniform(double v) { return v; }
+// the reduction of v over the token's LPT lanes, in every one of them (in a
+// scalar register where they are the whole wave, so branches on it are scalar)
 template <int LPT, typename T, typename F>
 __device__ __forceinline__ T over_token(T v, F f) {
   v = f(v, turn<8>(v));
   v = f(v, turn<4>(v));
   v = f(v, turn<2>(v));
   v = f(v, turn<1>(v));
-  if constexpr (LPT >= 32) v = f(v, turn<16>(v));
-  if constexpr (LPT >= 64) v = f(v, turn<32>(v));
+  if constexpr (LPT >= 32) v = across<16>(v, f);
+  if constexpr (LPT >= 64) v = uniform(across<32>(v, f));
   return v;
 }
 // v of the token's lane g
@@ -115,40 +169,29 @@ __device__ __forceinline__ T from_lane(T v, int g) {
   return __shfl(v, g, LPT);
 }
 
-// ------------------------------------------------------------------- groups
-// The open groups of one token as a bit mask, from selection values val[E] in
-// LDS (-inf: cannot be chosen).  `err(v)` bounds the error of a group's value;
-// near is set where the last open and the first closed group are closer.
-template <int LPT, typename F, typename Err>
-__device__ __forceinline__ uint64_t open_groups(const F* val, const RouteArgs& a, int g, F* gv,
-                                                Err err, bool& near) {
-  const F none = -__builtin_inf();
-  for (int q = g; q < a.G; q += LPT) {
-    F m1 = none, m2 = none;
-    int i = q % a.gsize;  // staggered starts keep the lanes on different LDS banks
-    for (int n = 0; n < a.gsize; ++n) {
-      const F v = val[q * a.gsize + i];
-      if (v > m1) {
-        m2 = m1;
-        m1 = v;
-      } else if (v > m2) {
-        m2 = v;
-      }
-      if (++i == a.gsize) i = 0;
-    }
-    gv[q] = (a.gtop == 2 && m2 > none) ? m1 + m2 : m1;
-  }
-  lds_sync();
+// e / gsize for e < 1024: (e * m) >> 20 with m = ceil(2^20 / gsize) is exact,
+// as e * (m * gsize - 2^20) <= 1023 * 1023 < 2^20
+__device__ __forceinline__ int group_of(int e, uint32_t magic) {
+  return static_cast<int>((static_cast<uint32_t>(e) * magic) >> 20);
+}
+
+// The open groups of one token as a bit mask, from the groups' values gv[G] in
+// LDS: fewer than tg are better (larger, or equal with a lower index).  last and
+// next: the smallest open and the largest closed value.
+template <int LPT, typename F>
+__device__ __forceinline__ uint64_t open_groups(const F* gv, int G, int tg, int g, F& last, F& next) {
   uint32_t lo = 0, hi = 0;
-  F last = __builtin_inf(), next = none;
-  for (int q = g; q < a.G; q += LPT) {
+  last = __builtin_inf();
+  next = -__builtin_inf();
+  for (int q = g; q < G; q += LPT) {
     const F v = gv[q];
     int better = 0;
-    for (int o = 0; o < a.G; ++o) {
+#pragma unroll 4
+    for (int o = 0; o < G; ++o) {
       const F u = gv[o];
       better += (u > v || (u == v && o < q)) ? 1 : 0;
     }
-    if (better < a.tg) {
+    if (better < tg) {
       if (q < 32) lo |= 1u << q;
       else hi |= 1u << (q - 32);
       last = v < last ? v : last;
@@ -156,75 +199,73 @@ __device__ __forceinline__ uint64_t open_groups(const F* val, const RouteArgs& a
       next = v > next ? v : next;
     }
   }
-  lo = over_token<LPT>(lo, [](uint32_t x, uint32_t y) { return x | y; });
-  hi = over_token<LPT>(hi, [](uint32_t x, uint32_t y) { return x | y; });
+  lo = over_token<LPT>(lo, Or());
+  if (G > 32) hi = over_token<LPT>(hi, Or());
   last = over_token<LPT>(last, Min());
   next = over_token<LPT>(next, Max());
-  // two infinities are equal values, and equal values go to the lowest index
-  near = next > none && last - next <= err(last) + err(next);
   return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 
-// e / gsize for e < 1024: (e * m) >> 20 with m = ceil(2^20 / gsize) is exact,
-// as e * (m * gsize - 2^20) <= 1023 * 1023 < 2^20
-__device__ __forceinline__ int group_of(int e, uint32_t magic) {
-  return static_cast<int>((static_cast<uint32_t>(e) * magic) >> 20);
-}
-
-// --------------------------------------------------------- binary64, in LDS
+// ----------------------------------------------------------------- binary64
 __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
 
-// The experts of selections g and g + LPT of a token, -1 where there is none.
-struct Chosen {
-  int lo = -1, hi = -1;
-  template <int LPT>
-  __device__ __forceinline__ void set(int k, int g, int e) {
-    if (k == g) lo = e;
-    if (LPT < 32 && k == g + LPT) hi = e;
+// Scores of one token's cleaned logits in binary64.
+struct Score64 {
+  bool sigmoid;
+  double lmax, sum;
+  __device__ __forceinline__ double operator()(float l) const {
+    return sigmoid ? sigmoid64(l) : exp(static_cast<double>(l) - lmax) / sum;
   }
-  __device__ __forceinline__ int operator[](int i) const { return i == 0 ? lo : hi; }
 };
-
-// One token again in binary64.  val [E], gv [kMaxRouteGroups] in LDS.
 template <int LPT, typename LT>
-__device__ __forceinline__ Chosen choose64(const RouteArgs& a, const LT* logits, int g, float lmax,
-                                        double* val, double* gv) {
+__device__ __forceinline__ Score64 score64(const RouteArgs& a, const LT* row, int g, float lmax) {
+  Score64 s = {a.sigmoid, static_cast<double>(lmax), 1.0};
+  if (!a.sigmoid) {
+    double sum = 0.0;
+    for (int e = g; e < a.E; e += LPT) {
+      const float l = clean_logit(raw_logit(row + e));
+      if (l > kNegInf) sum += exp(static_cast<double>(l) - s.lmax);
+    }
+    s.sum = over_token<LPT>(sum, Sum());
+  }
+  return s;
+}
+
+// The experts a token has chosen: s_idx[K] in LDS, -1 where there is none.
+// The whole of it in binary64: val [E], gv [kMaxRouteGroups] in LDS.
+template <int LPT, typename LT>
+__device__ __forceinline__ void choose64(const RouteArgs& a, const LT* row, int g, float lmax,
+                                         double* val, double* gv, int* s_idx) {
   const double none = -__builtin_inf();
   const int E = a.E;
-  double sum = 0.0;
-  if (!a.sigmoid) {
-    for (int e = g; e < E; e += LPT) {
-      const float l = clean_logit(raw_logit(logits + e));
-      if (l > kNegInf) sum += exp(static_cast<double>(l) - static_cast<double>(lmax));
-    }
-    sum = over_token<LPT>(sum, Sum());
-  }
-  auto score = [&](float l) {
-    return a.sigmoid ? sigmoid64(l) : exp(static_cast<double>(l) - static_cast<double>(lmax)) / sum;
-  };
+  const Score64 score = score64<LPT>(a, row, g, lmax);
   uint64_t open = ~0ull;
   const uint32_t magic = a.G ? ((1u << 20) + a.gsize - 1) / a.gsize : 0u;
   if (a.G) {
     const bool by_logit = !a.bias && a.gtop == 1;
-    for (int e = g; e < E; e += LPT) {
-      const float l = clean_logit(raw_logit(logits + e));
-      double v = by_logit ? static_cast<double>(l) : score(l) + (a.bias ? static_cast<double>(a.bias[e]) : 0.0);
-      if (l == kNegInf || v != v) v = none;
-      val[e] = v;
+    for (int q = g; q < a.G; q += LPT) {
+      double m1 = none, m2 = none;
+      for (int e = q * a.gsize; e < (q + 1) * a.gsize; ++e) {
+        const float l = clean_logit(raw_logit(row + e));
+        double v = by_logit ? static_cast<double>(l) : score(l) + (a.bias ? static_cast<double>(a.bias[e]) : 0.0);
+        if (l == kNegInf || v != v) v = none;
+        m2 = v > m1 ? m1 : v > m2 ? v : m2;
+        m1 = v > m1 ? v : m1;
+      }
+      gv[q] = (a.gtop == 2 && m2 > none) ? m1 + m2 : m1;
     }
     lds_sync();
-    bool near;
-    open = open_groups<LPT>(val, a, g, gv, [](double) { return 0.0; }, near);
+    double last, next;
+    open = open_groups<LPT>(gv, a.G, a.tg, g, last, next);
     lds_sync();
   }
   for (int e = g; e < E; e += LPT) {
-    const float l = clean_logit(raw_logit(logits + e));
+    const float l = clean_logit(raw_logit(row + e));
     double v = a.bias ? score(l) + static_cast<double>(a.bias[e]) : static_cast<double>(l);
     if (l == kNegInf || v != v || (a.G && !((open >> group_of(e, magic)) & 1))) v = none;
     val[e] = v;
   }
   lds_sync();
-  Chosen chosen;
   for (int k = 0; k < a.K; ++k) {
     double best = none;
     int at = INT32_MAX;
@@ -238,245 +279,430 @@ __device__ __forceinline__ Chosen choose64(const RouteArgs& a, const LT* logits,
     const double top = over_token<LPT>(best, Max());
     const uint32_t mine = (best == top && best > none) ? static_cast<uint32_t>(at) : UINT32_MAX;
     const uint32_t win = over_token<LPT>(mine, Min());
-    if (win == UINT32_MAX) break;
-    if (static_cast<int>(win) % LPT == g) val[win] = none;
+    const int e = win == UINT32_MAX ? -1 : static_cast<int>(win);
+    if (e >= 0 && e % LPT == g) val[e] = none;
+    if (g == 0) s_idx[k] = e;
     lds_sync();
-    chosen.template set<LPT>(k, g, static_cast<int>(win));
   }
-  return chosen;
 }
 
 // ------------------------------------------------------------------ forward
-// KEY32: bf16 logits without a bias, whose key fits 32 bits.
-template <int LPT, int NV, typename LT, bool KEY32>
-__global__ __launch_bounds__(kWave) void k_route(RouteArgs a, int64_t waves) {
-  constexpr int kTok = kWave / LPT;  // tokens per wave
-  constexpr int kCap = LPT * NV;     // experts a token's lanes hold
-  __shared__ double s_val[kTok * kCap];
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// Batcher's odd-even merge sort, descending.
+template <int N>
+__device__ __forceinline__ void sort_descending(uint32_t (&k)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j <= N - 1 - q; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const uint32_t x = k[i + j], y = k[i + j + q];
+            k[i + j] = x > y ? x : y;
+            k[i + j + q] = x > y ? y : x;
+          }
+}
+
+// The N largest of k[0..M), descending.
+template <int M, int N>
+__device__ __forceinline__ void keep_largest(uint32_t (&k)[M], uint32_t (&out)[N]) {
+  if constexpr (M == N) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = k[i];
+    sort_descending(out);
+  } else {
+    static_assert(M == 2 * N, "two halves");
+    uint32_t x[N], y[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      x[i] = k[i];
+      y[i] = k[N + i];
+    }
+    sort_descending(x);
+    sort_descending(y);
+    // the larger of x[i] and y[N - 1 - i] are the N largest, a bitonic run
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = x[i] > y[N - 1 - i] ? x[i] : y[N - 1 - i];
+#pragma unroll
+    for (int d = N / 2; d >= 1; d /= 2)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if ((i & d) == 0) {
+          const uint32_t u = out[i], v = out[i + d];
+          out[i] = u > v ? u : v;
+          out[i + d] = u > v ? v : u;
+        }
+  }
+}
+
+__host__ __device__ constexpr int log2i(int n) { return n <= 1 ? 0 : 1 + log2i(n / 2); }
+
+// What experts are compared by: bf16 logits (exact in a key), fp32 logits, or
+// score + bias.
+enum { kByBf16, kByFp32, kByScore };
+
+// KEEP: keys a lane keeps sorted, NV or (K <= 8) half of 16.
+template <int LPT, int NV, int KEEP, typename LT, int BY>
+__global__ __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) void k_route(
+    RouteArgs a) {
+  constexpr int kTok = kWave / LPT;             // tokens per wave
+  constexpr int kCap = LPT * NV;                // experts a token's lanes hold
+  constexpr int kCand = LPT >= 32 ? 64 : 48;    // candidates kept, more than K
+  constexpr int kOut = LPT >= 32 ? 1 : 2;       // selections per lane
+  constexpr int kLow = BY == kByBf16 ? 16 : log2i(NV);  // index bits of a key
+  constexpr uint32_t kLowMask = (1u << kLow) - 1;
+  constexpr int kPitch = kCap + 32 > 2 * kCand ? kCap + 32 : 2 * kCand;
+  static_assert(kTok * kPitch >= 2 * kCap || kTok == 1, "choose64's values");
+  __shared__ __align__(8) float s_val[kTok * kPitch > 2 * kCap ? kTok * kPitch : 2 * kCap];
   __shared__ double s_gv[kTok * kMaxRouteGroups];
+  __shared__ uint32_t s_key[kTok][kCand];
+  __shared__ int s_idx[kTok][kCand];
   const int lane = threadIdx.x;
   const int g = lane % LPT;
   const int tok = lane / LPT;
   const int E = a.E, K = a.K;
   const LT* all = static_cast<const LT*>(a.logits);
-  float* valf = reinterpret_cast<float*>(s_val + tok * kCap);
-  float* gvf = reinterpret_cast<float*>(s_gv + tok * kMaxRouteGroups);
+  float* valf = s_val + tok * kPitch;                     // one token's values
+  double* cand = reinterpret_cast<double*>(valf);          // or its candidates'
+  double* gv = s_gv + tok * kMaxRouteGroups;
+  float* gvf = reinterpret_cast<float*>(gv);
+  uint32_t* keys = s_key[tok];
+  int* idxs = s_idx[tok];
   const uint32_t magic = a.G ? ((1u << 20) + a.gsize - 1) / a.gsize : 0u;
-  const bool vec = E % 4 == 0 && (reinterpret_cast<uintptr_t>(all) & (4 * sizeof(LT) - 1)) == 0;
-  const bool scored = a.bias != nullptr;  // experts compared by score + bias
-  const bool need_scores = scored || (a.G && a.gtop == 2);
+  const bool vec = E % 4 == 0 && (reinterpret_cast<uintptr_t>(all) & (4 * sizeof(LT) - 1)) == 0 &&
+                   (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0;
+  const bool group_scores = a.G && (BY == kByScore || a.gtop == 2);
+  const bool need_scores = BY == kByScore || group_scores;
   const bool need_sum = !a.sigmoid && (need_scores || !a.renorm);
 
-  for (int64_t wv = blockIdx.x; wv < waves; wv += gridDim.x) {
-    const int64_t t = wv * kTok + tok;
-    if (t >= a.T) continue;  // whole groups of LPT lanes: the reductions stay within a token
-    const LT* row = all + t * E;
-    Chosen chosen;
-    const bool masked = a.mask && a.mask[t] == 0;
-    float lmax = kNegInf, lsum = 1.0f;
-    if (!masked) {
-      float l[NV];
+  const int64_t t = wave_task() * kTok + tok;
+  if (t >= a.T) return;  // whole groups of LPT lanes: the reductions stay within a token
+  const LT* row = all + t * E;
+  const bool masked = a.mask && a.mask[t] == 0;
+  float lmax = kNegInf, lsum = 1.0f;
+  int chosen[kOut];
 #pragma unroll
-      for (int j = 0; j < NV / 4; ++j) {
-        const int e0 = j * 4 * LPT + 4 * g;
-        if (vec) {
-          if (e0 < E) {
-            if constexpr (sizeof(LT) == 4) {
-              const u32x4 v = *reinterpret_cast<const u32x4*>(row + e0);
+  for (int i = 0; i < kOut; ++i) chosen[i] = -1;
+  if (!masked) {
+    float l[NV], bias[BY == kByScore ? NV : 1];
 #pragma unroll
-              for (int c = 0; c < 4; ++c) l[4 * j + c] = __uint_as_float(v[c]);
-            } else {
-              const u32x2 v = *reinterpret_cast<const u32x2*>(row + e0);
-              l[4 * j] = bf16_lo(v[0]);
-              l[4 * j + 1] = bf16_hi(v[0]);
-              l[4 * j + 2] = bf16_lo(v[1]);
-              l[4 * j + 3] = bf16_hi(v[1]);
-            }
-          } else {
+    for (int j = 0; j < NV / 4; ++j) {
+      const int e0 = j * 4 * LPT + 4 * g;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) l[4 * j + c] = kNegInf;
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) l[4 * j + c] = e0 + c < E ? raw_logit(row + e0 + c) : kNegInf;
-        }
+      for (int c = 0; c < 4; ++c) {
+        l[4 * j + c] = kNegInf;
+        if constexpr (BY == kByScore) bias[4 * j + c] = 0.0f;
       }
+      if (vec) {
+        if (e0 < E) {
+          if constexpr (BY == kByScore) {
+            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(a.bias + e0);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) bias[4 * j + c] = v[c];
+          }
+          if constexpr (sizeof(LT) == 4) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(row + e0);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) l[4 * j + c] = __uint_as_float(v[c]);
+          } else {
+            const u32x2 v = *reinterpret_cast<const u32x2*>(row + e0);
+            l[4 * j] = bf16_lo(v[0]);
+            l[4 * j + 1] = bf16_hi(v[0]);
+            l[4 * j + 2] = bf16_lo(v[1]);
+            l[4 * j + 3] = bf16_hi(v[1]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (e0 + c < E) {
+            l[4 * j + c] = raw_logit(row + e0 + c);
+            if constexpr (BY == kByScore) bias[4 * j + c] = a.bias[e0 + c];
+          }
+      }
+    }
+    auto expert = [&](int i) { return (i / 4) * 4 * LPT + 4 * g + i % 4; };
+    uint32_t all_keys[NV];
+    auto make_key = [&](int i, float v) {
+      return v > kNegInf ? (ordered(v) & ~kLowMask) | (kLowMask - static_cast<uint32_t>(BY == kByBf16 ? expert(i) : i)) : 0u;
+    };
+    if constexpr (BY == kByBf16) {
+      // NaN is left out by the comparison; +inf stays above the largest bf16
+#pragma unroll
+      for (int i = 0; i < NV; ++i) all_keys[i] = make_key(i, l[i] + 0.0f);
+    }
+    if (BY != kByBf16 || a.G || need_sum) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) l[i] = clean_logit(l[i]);
-      auto expert = [&](int i) { return (i / 4) * 4 * LPT + 4 * g + i % 4; };
+    }
+    if constexpr (BY == kByFp32) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) all_keys[i] = make_key(i, l[i]);
+    }
 
-      if (need_sum) {
-        float m = l[0];
+    if (need_sum) {
+      float m = l[0];
 #pragma unroll
-        for (int i = 1; i < NV; ++i) m = fmaxf(m, l[i]);
-        lmax = over_token<LPT>(m, Max());
-        float s = 0.0f;
-        if (lmax > kNegInf) {
-#pragma unroll
-          for (int i = 0; i < NV; ++i) s += expf(l[i] - lmax);
-        }
-        lsum = over_token<LPT>(s, Sum());
-      }
-
-      // selection values, and the bound on their error: a score's relative
-      // error is below 2^-21 for the sigmoid (exponential, sum, quotient: 4
-      // roundings) and 2^-17 for the softmax (the rounded exponent l - max,
-      // up to 88, adds 88 * 2^-24); adding the bias is one more rounding
-      float c[KEY32 ? 1 : NV];
-      float bmax = 0.0f;
-      if constexpr (!KEY32) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) c[i] = l[i];
-      }
-      const float rel = a.sigmoid ? 0x1p-21f : 0x1p-17f;
-      bool near = false;
-      uint64_t open = ~0ull;
-      if (need_scores) {
-        float score[NV];
+      for (int i = 1; i < NV; ++i) m = fmaxf(m, l[i]);
+      lmax = over_token<LPT>(m, Max());
+    }
+    // Scores for the comparisons, with the hardware's exponential and
+    // reciprocal (1 ulp each).  An exponent x is off by at most 2.5 |x| 2^-24,
+    // |x| <= 88 where the result counts, so a score's relative error is below
+    // (2.5 * 88 + 30) 2^-24 < 2^-16; as exp(x) |x| <= 0.37 for x < 0, its
+    // absolute error is below 7 * 2^-24 for the sigmoid, and for the softmax,
+    // whose sum is off by the average of its terms, below 61 * 2^-24.
+    float c[NV];
+    float bmax = 0.0f;
+    if (need_sum) {
+      float s = 0.0f;
+      if (lmax > kNegInf) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          float v = a.sigmoid ? 1.0f / (1.0f + expf(-l[i])) : expf(l[i] - lmax) / lsum;
-          if (scored) {
-            const float b = expert(i) < E ? a.bias[expert(i)] : 0.0f;
-            if (fabsf(b) < __builtin_inff()) bmax = fmaxf(bmax, fabsf(b));
-            v += b;
-          }
-          score[i] = (l[i] == kNegInf || v != v) ? kNegInf : v;
+          // the weights that are not renormalised need the sum to fp32's accuracy
+          c[i] = a.renorm ? __builtin_amdgcn_exp2f((l[i] - lmax) * kLog2e) : expf(l[i] - lmax);
+          s += c[i];
         }
-        if (scored) {
-          bmax = over_token<LPT>(bmax, Max());
-          if constexpr (!KEY32) {
+      }
+      lsum = over_token<LPT>(s, Sum());
+    }
+    if (need_scores) {
+      const float inv = __builtin_amdgcn_rcpf(lsum);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) c[i] = score[i];
-          }
+      for (int i = 0; i < NV; ++i) {
+        float v = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-l[i] * kLog2e)) : c[i] * inv;
+        if constexpr (BY == kByScore) {
+          if (fabsf(bias[i]) < __builtin_inff()) bmax = fmaxf(bmax, fabsf(bias[i]));
+          v += bias[i];
         }
-        if (a.G) {
+        c[i] = (l[i] == kNegInf || v != v) ? kNegInf : v;
+      }
+      if constexpr (BY == kByScore) bmax = over_token<LPT>(bmax, Max());
+    }
+    // bounds on the error of a value, score + bias, and of a sum of two
+    const float cap = a.sigmoid ? 0x1p-21f : 0x1p-18f;
+    auto err = [&](float v) {
+      return fminf(cap, 0x1p-16f * (fabsf(v) + bmax)) + 0x1p-22f * fabsf(v) + 1e-37f;
+    };
+    auto err2 = [&](float v) {
+      return fminf(2.0f * cap, 0x1p-16f * (fabsf(v) + 2.0f * bmax)) + 0x1p-22f * (fabsf(v) + 4.0f * bmax) + 2e-37f;
+    };
+
+    uint64_t open = ~0ull;
+    bool doubt = false;
+    if (a.G) {
 #pragma unroll
-          for (int i = 0; i < NV; ++i)
-            if (expert(i) < E) valf[expert(i)] = score[i];
+      for (int i = 0; i < NV; ++i)
+        if (expert(i) < E) valf[expert(i)] = group_scores ? c[i] : l[i];
+      lds_sync();
+      // P lanes read one group, each every Pth value from a start that
+      // keeps the groups on different banks
+      const int P = a.G * 4 <= LPT && a.gsize % 4 == 0 ? 4 : a.G * 2 <= LPT && a.gsize % 2 == 0 ? 2 : 1;
+      const int sub = g % P;
+      for (int q = g / P; q < a.G; q += LPT / P) {
+        float m1 = kNegInf, m2 = kNegInf;
+        int at = (q * P) % a.gsize;
+        at = at - at % P + sub;
+#pragma unroll 4
+        for (int n = 0; n < a.gsize; n += P) {
+          const float v = valf[q * a.gsize + at];
+          at += P;
+          if (at >= a.gsize) at -= a.gsize;
+          m2 = __builtin_amdgcn_fmed3f(m1, m2, v);  // m1 >= m2
+          m1 = fmaxf(m1, v);
         }
-      } else if (a.G) {
+        for (int off = 1; off < P; off <<= 1) {
+          const float o1 = __shfl_xor(m1, off, kWave), o2 = __shfl_xor(m2, off, kWave);
+          m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+          m1 = fmaxf(m1, o1);
+        }
+        if (sub == 0) gvf[q] = (a.gtop == 2 && m2 > kNegInf) ? m1 + m2 : m1;
+      }
+      lds_sync();
+      float last, next;
+      open = open_groups<LPT>(gvf, a.G, a.tg, g, last, next);
+      lds_sync();
+      if (group_scores && next > kNegInf && last - next <= err2(last) + err2(next)) {
+        // the groups' values in binary64: each group's best one or two,
+        // found by their fp32 values, if those leave no doubt
+        const Score64 score = score64<LPT>(a, row, g, lmax);
+        auto exact = [&](int e) {
+          return score(clean_logit(raw_logit(row + e))) + (BY == kByScore ? static_cast<double>(a.bias[e]) : 0.0);
+        };
+        for (int q = g; q < a.G; q += LPT) {
+          float m1 = kNegInf, m2 = kNegInf, m3 = kNegInf;
+          int e1 = -1, e2 = -1;
+          for (int n = 0; n < a.gsize; ++n) {
+            const float v = valf[q * a.gsize + n];
+            if (v > m1) {
+              m3 = m2;
+              m2 = m1;
+              e2 = e1;
+              m1 = v;
+              e1 = q * a.gsize + n;
+            } else if (v > m2) {
+              m3 = m2;
+              m2 = v;
+              e2 = q * a.gsize + n;
+            } else if (v > m3) {
+              m3 = v;
+            }
+          }
+          const float in = a.gtop == 2 ? m2 : m1, out = a.gtop == 2 ? m3 : m2;
+          if (out > kNegInf && in - out <= err(in) + err(out)) doubt = true;
+          double v = -__builtin_inf();
+          if (e1 >= 0) v = exact(e1);
+          if (a.gtop == 2 && e2 >= 0) v += exact(e2);
+          gv[q] = v;
+        }
+        lds_sync();
+        double last64, next64;
+        open = open_groups<LPT>(gv, a.G, a.tg, g, last64, next64);
+        doubt = over_token<LPT>(doubt ? 1u : 0u, Or()) != 0u;
+        lds_sync();
+      }
+    }
+
+    if constexpr (BY == kByScore) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) all_keys[i] = make_key(i, c[i]);
+    }
+    if (a.G) {
+      if (a.gsize % 4 == 0) {  // four neighbours share a group
+#pragma unroll
+        for (int j = 0; j < NV / 4; ++j) {
+          const bool shut = !((open >> group_of(expert(4 * j), magic)) & 1);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) all_keys[4 * j + c] = shut ? 0u : all_keys[4 * j + c];
+        }
+      } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if (expert(i) < E) valf[expert(i)] = l[i];
+          all_keys[i] = (open >> group_of(expert(i), magic)) & 1 ? all_keys[i] : 0u;
       }
-      auto err = [&](float v) {
-        return rel * fminf(1.0f, fabsf(v) + bmax) + 0x1p-23f * fabsf(v) + 1e-37f;
-      };
-      if (a.G) {
-        lds_sync();
-        if (need_scores) {
-          // a sum of two values: twice the bound, and the sum's rounding
-          open = open_groups<LPT>(valf, a, g, gvf, [&](float v) {
-            return 2.0f * (rel * fminf(1.0f, fabsf(v) + 2.0f * bmax) + 0x1p-22f * (fabsf(v) + bmax) + 1e-37f);
-          }, near);
-        } else {
-          open = open_groups<LPT>(valf, a, g, gvf, [](float) { return 0.0f; }, near);
-          near = false;  // logits are exact: equal groups go to the lowest index
-        }
-        lds_sync();
-      }
-
-      if (!near) {
-        // keys: the ordered value above the complement of the index; 0 = none
-        if constexpr (KEY32) {
-          uint32_t key[NV];
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const int e = expert(i);
-            const bool ok = l[i] > kNegInf && (!a.G || ((open >> group_of(e, magic)) & 1));
-            // only +inf, cleaned, reaches the largest finite fp32 here: it
-            // stays above the largest bf16
-            const uint32_t value = l[i] >= FLT_MAX ? 0xFF800000u : ordered(l[i]) & 0xFFFF0000u;
-            key[i] = ok ? value | (0xFFFFu - static_cast<uint32_t>(e)) : 0u;
-          }
-          for (int k = 0; k < K; ++k) {
-            uint32_t m = key[0];
-#pragma unroll
-            for (int i = 1; i < NV; ++i) m = m > key[i] ? m : key[i];
-            m = over_token<LPT>(m, Max());
-            if (m == 0u) break;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) key[i] = key[i] == m ? 0u : key[i];
-            chosen.template set<LPT>(k, g, static_cast<int>(0xFFFFu - (m & 0xFFFFu)));
-          }
-        } else {
-          uint64_t key[NV];
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const int e = expert(i);
-            const bool ok = c[i] > kNegInf && (!a.G || ((open >> group_of(e, magic)) & 1));
-            key[i] = ok ? (static_cast<uint64_t>(ordered(c[i])) << 32) | ~static_cast<uint32_t>(e) : 0ull;
-          }
-          float prev = 0.0f;
-          int prev_e = -1;
-          // one round more than K: the first expert left out must be clear of the last chosen
-          for (int k = 0; k < K + (scored ? 1 : 0); ++k) {
-            uint64_t m = key[0];
-#pragma unroll
-            for (int i = 1; i < NV; ++i) m = m > key[i] ? m : key[i];
-            m = over_token<LPT>(m, Max());
-            if (m == 0ull) break;
-            const int e = static_cast<int>(~static_cast<uint32_t>(m));
-            if (scored) {
-              const float v = unordered(static_cast<uint32_t>(m >> 32));
-              if (prev_e >= 0 && prev - v <= err(prev) + err(v)) {
-                // values of one and the same logit and bias are equal in binary64 too
-                const bool same = raw_logit(row + e) == raw_logit(row + prev_e) && a.bias[e] == a.bias[prev_e];
-                if (!same) near = true;
-              }
-              prev = v;
-              prev_e = e;
-            }
-            if (k == K || near) break;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) key[i] = key[i] == m ? 0ull : key[i];
-            chosen.template set<LPT>(k, g, e);
-          }
-        }
-      }
-      if (near) chosen = choose64<LPT>(a, row, g, lmax, s_val + tok * kCap, s_gv + tok * kMaxRouteGroups);
     }
-
-    // weights of selections g and g + LPT
-    constexpr int kSlots = LPT >= 32 ? 1 : 2;
-    float lc[kSlots], w[kSlots];
-    float top = kNegInf;
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
-      lc[i] = chosen[i] >= 0 ? clean_logit(raw_logit(row + chosen[i])) : kNegInf;
-      top = fmaxf(top, lc[i]);
-    }
-    if (a.renorm) {
-      // relative to the largest: softmax exp(l - top); sigmoid(l) =
-      // exp(-log(1 + exp(-l)))
-      top = over_token<LPT>(top, Max());
-      const float ltop = fminf(top, 0.0f) - log1pf(expf(-fabsf(top)));
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        float e = 0.0f;
-        if (chosen[i] >= 0) {
-          e = a.sigmoid ? expf(fminf(lc[i], 0.0f) - log1pf(expf(-fabsf(lc[i]))) - ltop) : expf(lc[i] - top);
+    uint32_t key[KEEP];
+    keep_largest(all_keys, key);
+    auto close = [&](uint32_t x, uint32_t y) {
+      const float u = unordered(x & ~kLowMask), v = unordered(y & ~kLowMask);
+      float tol = 0x1p-22f * (1u << kLow) * fabsf(v) + 1e-37f;
+      if (BY == kByScore) tol += err(u) + err(v);
+      return u - v <= tol;
+    };
+    const uint64_t before = lanemask_lt() & ~((1ull << (tok * LPT)) - 1);  // the token's lanes below this one
+    uint32_t prev = 0;
+    int taken = 0;  // of this lane's keys
+    int count = 0;  // candidates, in the same order in all of the token's lanes
+    while (!doubt) {
+      const uint32_t m = over_token<LPT>(key[0], Max());
+      if (m == 0u) break;
+      if (count >= K) {
+        if (BY == kByBf16 || !close(prev, m)) break;
+        if (count == kCand) {
+          doubt = true;
+          break;
         }
-        w[i] = e;
-        sum += e;
       }
-      sum = over_token<LPT>(sum, Sum());
+      bool mine = key[0] == m;
+      if (BY == kByBf16) {
+        if (mine) idxs[count] = static_cast<int>(kLowMask - (m & kLowMask));
+      } else {
+        mine = mine && (ballot(mine) & before) == 0;  // the lowest lane of equal keys
+        if (mine) {
+          keys[count] = m;
+          idxs[count] = expert(static_cast<int>(kLowMask - (m & kLowMask)));
+        }
+      }
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i) w[i] = w[i] / sum * a.scale;
+      for (int i = 0; i < KEEP - 1; ++i) key[i] = mine ? key[i + 1] : key[i];
+      key[KEEP - 1] = mine ? 0u : key[KEEP - 1];
+      prev = m;
+      ++count;
+      if (BY == kByBf16) {
+        if (count == K) break;
+      } else if (KEEP < NV) {
+        taken += mine ? 1 : 0;
+      }
+    }
+    // a lane whose kept keys are used up may have had another
+    if (BY != kByBf16 && KEEP < NV) doubt |= over_token<LPT>(taken == KEEP ? 1u : 0u, Or()) != 0u;
+    lds_sync();
+    bool near = false;  // the candidates were put in order by their exact values: in keys
+    if (BY != kByBf16 && !doubt) {
+      for (int k = g; k < count - 1; k += LPT) near |= close(keys[k], keys[k + 1]);
+      near = over_token<LPT>(near ? 1u : 0u, Or()) != 0u;
+      if (near) {
+        // the candidates' exact values, and each one's place among them
+        Score64 score = {};
+        if (BY == kByScore) score = score64<LPT>(a, row, g, lmax);
+        for (int k = g; k < count; k += LPT) {
+          const int e = idxs[k];
+          const float x = clean_logit(raw_logit(row + e));
+          cand[k] = BY == kByScore ? score(x) + static_cast<double>(a.bias[e]) : static_cast<double>(x);
+        }
+        lds_sync();
+        for (int k = g; k < count; k += LPT) {
+          const double v = cand[k];
+          const int e = idxs[k];
+          int place = 0;
+#pragma unroll 4
+          for (int j = 0; j < count; ++j) place += (cand[j] > v || (cand[j] == v && idxs[j] < e)) ? 1 : 0;
+          keys[place] = static_cast<uint32_t>(e);
+        }
+        lds_sync();
+      }
+    }
+    if (doubt) {
+      // one token after the other: its values take the whole array
+      for (int d = 0; d < kTok; ++d)
+        if (d == tok) choose64<LPT>(a, row, g, lmax, reinterpret_cast<double*>(s_val), gv, idxs);
+#pragma unroll
+      for (int i = 0; i < kOut; ++i)
+        if (g + i * LPT < K) chosen[i] = idxs[g + i * LPT];
     } else {
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i)
-        w[i] = (a.sigmoid ? 1.0f / (1.0f + expf(-lc[i])) : expf(lc[i] - lmax) / lsum) * a.scale;
-    }
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
-      const int k = g + i * LPT;
-      if (k < K) {
-        a.idx[t * K + k] = chosen[i];
-        a.w[t * K + k] = chosen[i] >= 0 ? w[i] : 0.0f;
+      for (int i = 0; i < kOut; ++i) {
+        const int k = g + i * LPT;
+        if (k < K && k < count) chosen[i] = near ? static_cast<int>(keys[k]) : idxs[k];
       }
+    }
+    lds_sync();
+  }
+
+  // weights of selections g and g + LPT
+  float lc[kOut], w[kOut];
+  float top = kNegInf;
+#pragma unroll
+  for (int i = 0; i < kOut; ++i) {
+    lc[i] = chosen[i] >= 0 ? clean_logit(raw_logit(row + chosen[i])) : kNegInf;
+    top = fmaxf(top, lc[i]);
+  }
+  if (a.renorm) {
+    top = over_token<LPT>(top, Max());
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kOut; ++i) {
+      w[i] = chosen[i] >= 0 ? relative_score(lc[i], top, a.sigmoid) : 0.0f;
+      sum += w[i];
+    }
+    sum = over_token<LPT>(sum, Sum());
+#pragma unroll
+    for (int i = 0; i < kOut; ++i) w[i] = w[i] / sum * a.scale;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kOut; ++i)
+      w[i] = (a.sigmoid ? sigmoid32(lc[i]) : expf(lc[i] - lmax) / lsum) * a.scale;
+  }
+#pragma unroll
+  for (int i = 0; i < kOut; ++i) {
+    const int k = g + i * LPT;
+    if (k < K) {
+      a.idx[t * K + k] = chosen[i];
+      a.w[t * K + k] = chosen[i] >= 0 ? w[i] : 0.0f;
     }
   }
 }
@@ -485,7 +711,7 @@ __global__ __launch_bounds__(kWave) void k_route(RouteArgs a, int64_t waves) {
 // Lane g of a token holds selections g and g + LPT; the gradient's row is put
 // together in LDS and written whole.
 template <int LPT, typename LT>
-__global__ __launch_bounds__(kWave) void k_route_backward(RouteArgs a, int64_t waves, int cap) {
+__global__ __launch_bounds__(kWave) void k_route_backward(RouteArgs a, int cap) {
   extern __shared__ float s_row[];  // [64 / LPT][cap]
   constexpr int kTok = kWave / LPT;
   constexpr int kSlots = LPT >= 32 ? 1 : 2;
@@ -498,161 +724,162 @@ __global__ __launch_bounds__(kWave) void k_route_backward(RouteArgs a, int64_t w
                    ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.glogits)) &
                     (4 * sizeof(LT) - 1)) == 0;
   const bool dense = !a.sigmoid && !a.renorm;
-  for (int64_t wv = blockIdx.x; wv < waves; wv += gridDim.x) {
-    const int64_t t = wv * kTok + tok;
-    if (t >= a.T) continue;
-    const LT* row = static_cast<const LT*>(a.logits) + t * E;
-    LT* out = static_cast<LT*>(a.glogits) + t * E;
+  const int64_t t = wave_task() * kTok + tok;
+  if (t >= a.T) return;
+  const LT* row = static_cast<const LT*>(a.logits) + t * E;
+  LT* out = static_cast<LT*>(a.glogits) + t * E;
 
-    for (int e = g; e < cap; e += LPT) d_row[e] = 0.0f;
-    int idx[kSlots];
-    float gw[kSlots], lc[kSlots], d[kSlots];
-    float top = kNegInf;
+  for (int e = g; e < cap; e += LPT) d_row[e] = 0.0f;
+  int idx[kSlots];
+  float gw[kSlots], lc[kSlots], d[kSlots];
+  float top = kNegInf;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const int k = g + i * LPT;
+    idx[i] = -1;
+    gw[i] = 0.0f;
+    if (k < K) {
+      const int64_t e = a.idx[t * K + k];
+      if (e >= 0 && e < E) {
+        idx[i] = static_cast<int>(e);
+        gw[i] = a.gw[t * K + k] * a.scale;
+      }
+    }
+    lc[i] = idx[i] >= 0 ? clean_logit(raw_logit(row + idx[i])) : kNegInf;
+    top = fmaxf(top, lc[i]);
+  }
+  if (a.renorm) {
+    top = over_token<LPT>(top, Max());
+    float w[kSlots];
+    float sum = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
-      const int k = g + i * LPT;
-      idx[i] = -1;
-      gw[i] = 0.0f;
-      if (k < K) {
-        const int64_t e = a.idx[t * K + k];
-        if (e >= 0 && e < E) {
-          idx[i] = static_cast<int>(e);
-          gw[i] = a.gw[t * K + k] * a.scale;
-        }
-      }
-      lc[i] = idx[i] >= 0 ? clean_logit(raw_logit(row + idx[i])) : kNegInf;
-      top = fmaxf(top, lc[i]);
+      w[i] = 0.0f;
+      if (lc[i] > kNegInf) w[i] = relative_score(lc[i], top, a.sigmoid);
+      sum += w[i];
     }
-    if (a.renorm) {
-      top = over_token<LPT>(top, Max());
-      const float ltop = fminf(top, 0.0f) - log1pf(expf(-fabsf(top)));
-      float w[kSlots];
-      float sum = 0.0f, dot = 0.0f;
+    sum = over_token<LPT>(sum, Sum());
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        w[i] = 0.0f;
-        if (lc[i] > kNegInf)
-          w[i] = a.sigmoid ? expf(fminf(lc[i], 0.0f) - log1pf(expf(-fabsf(lc[i]))) - ltop) : expf(lc[i] - top);
-        sum += w[i];
-      }
-      sum = over_token<LPT>(sum, Sum());
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        w[i] = sum > 0.0f ? w[i] / sum : 0.0f;
-        if (idx[i] >= 0) dot += w[i] * gw[i];
-      }
-      dot = over_token<LPT>(dot, Sum());
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        d[i] = w[i] * (gw[i] - dot);
-        if (a.sigmoid) d[i] *= 1.0f / (1.0f + expf(lc[i]));
-      }
-    } else if (a.sigmoid) {
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i) d[i] = gw[i] / (1.0f + expf(lc[i])) * (1.0f / (1.0f + expf(-lc[i])));
-    } else {
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i) d[i] = gw[i];
+    for (int i = 0; i < kSlots; ++i) {
+      w[i] = sum > 0.0f ? w[i] / sum : 0.0f;
+      if (idx[i] >= 0) dot += w[i] * gw[i];
     }
+    dot = over_token<LPT>(dot, Sum());
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-      if (idx[i] < 0 || lc[i] == kNegInf) d[i] = 0.0f;
-    // an expert named more than once: each of its selections carries the sum
-    // of their terms in ascending k, so they write the same value
-    float total[kSlots];
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) total[i] = 0.0f;
-    for (int k = 0; k < K; ++k) {
-      const int from = k % LPT;
-      const bool second = kSlots > 1 && k >= LPT;
-      const int ek = from_lane<LPT>(second ? idx[kSlots - 1] : idx[0], from);
-      const float dk = from_lane<LPT>(second ? d[kSlots - 1] : d[0], from);
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i) total[i] += ek == idx[i] ? dk : 0.0f;
+    for (int i = 0; i < kSlots; ++i) {
+      d[i] = w[i] * (gw[i] - dot);
+      if (a.sigmoid) d[i] *= sigmoid32(-lc[i]);
     }
-    lds_sync();
+  } else if (a.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-      if (idx[i] >= 0) d_row[idx[i]] = total[i];
-    lds_sync();
+    for (int i = 0; i < kSlots; ++i) d[i] = gw[i] * sigmoid32(-lc[i]) * sigmoid32(lc[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) d[i] = gw[i];
+  }
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i)
+    if (idx[i] < 0 || lc[i] == kNegInf) d[i] = 0.0f;
+  // an expert named more than once: each of its selections carries the sum
+  // of their terms in ascending k, so they write the same value
+  float total[kSlots];
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) total[i] = 0.0f;
+  for (int k = 0; k < K; ++k) {
+    const int from = k % LPT;
+    const bool second = kSlots > 1 && k >= LPT;
+    const int ek = from_lane<LPT>(second ? idx[kSlots - 1] : idx[0], from);
+    const float dk = from_lane<LPT>(second ? d[kSlots - 1] : d[0], from);
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) total[i] += ek == idx[i] ? dk : 0.0f;
+  }
+  lds_sync();
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i)
+    if (idx[i] >= 0) d_row[idx[i]] = total[i];
+  lds_sync();
 
-    float m = kNegInf, inv = 0.0f, dot = 0.0f;
-    if (dense) {
-      for (int e = g; e < E; e += LPT) m = fmaxf(m, clean_logit(raw_logit(row + e)));
-      m = over_token<LPT>(m, Max());
-      float s = 0.0f;
-      if (m > kNegInf) {
-        for (int e = g; e < E; e += LPT) {
-          const float x = expf(clean_logit(raw_logit(row + e)) - m);
-          s += x;
-          dot += x * d_row[e];
-        }
-      }
-      s = over_token<LPT>(s, Sum());
-      dot = over_token<LPT>(dot, Sum());
-      inv = s > 0.0f ? 1.0f / s : 0.0f;
-      dot *= inv;
-    }
-    auto value = [&](int e) {
-      const float dv = d_row[e];
-      if (!dense) return dv;
-      const float l = clean_logit(raw_logit(row + e));
-      return l > kNegInf ? expf(l - m) * inv * (dv - dot) : 0.0f;
-    };
-    if (vec) {
-      for (int e = 4 * g; e < E; e += 4 * LPT) {
-        const float v0 = value(e), v1 = value(e + 1), v2 = value(e + 2), v3 = value(e + 3);
-        if constexpr (sizeof(LT) == 4) {
-          u32x4 v;
-          v[0] = __float_as_uint(v0);
-          v[1] = __float_as_uint(v1);
-          v[2] = __float_as_uint(v2);
-          v[3] = __float_as_uint(v3);
-          *reinterpret_cast<u32x4*>(out + e) = v;
-        } else {
-          u32x2 v;
-          v[0] = bf16x2_of(v0, v1);
-          v[1] = bf16x2_of(v2, v3);
-          *reinterpret_cast<u32x2*>(out + e) = v;
-        }
-      }
-    } else {
+  float m = kNegInf, inv = 0.0f, dot = 0.0f;
+  if (dense) {
+    for (int e = g; e < E; e += LPT) m = fmaxf(m, clean_logit(raw_logit(row + e)));
+    m = over_token<LPT>(m, Max());
+    float s = 0.0f;
+    if (m > kNegInf) {
       for (int e = g; e < E; e += LPT) {
-        if constexpr (sizeof(LT) == 4) out[e] = value(e);
-        else out[e] = bf16_of(value(e));
+        const float x = expf(clean_logit(raw_logit(row + e)) - m);
+        s += x;
+        dot += x * d_row[e];
       }
     }
-    lds_sync();
+    s = over_token<LPT>(s, Sum());
+    dot = over_token<LPT>(dot, Sum());
+    inv = s > 0.0f ? 1.0f / s : 0.0f;
+    dot *= inv;
   }
-}
-
-// Blocks (one wave each) for `waves` wave tasks; the kernels walk them
-// cyclically, so a capped grid still covers them.
-unsigned route_blocks(int64_t waves) {
-  constexpr int64_t kMaxBlocks = 1 << 22;
-  return static_cast<unsigned>(waves < kMaxBlocks ? waves : kMaxBlocks);
-}
-
-template <int LPT, int NV, typename LT>
-hipError_t route_k(const RouteArgs& a, hipStream_t s) {
-  const int64_t waves = (a.T + kWave / LPT - 1) / (kWave / LPT);
-  if constexpr (sizeof(LT) == 2) {
-    if (!a.bias) {
-      k_route<LPT, NV, LT, true><<<route_blocks(waves), kWave, 0, s>>>(a, waves);
-      return hipGetLastError();
+  auto value = [&](int e) {
+    const float dv = d_row[e];
+    if (!dense) return dv;
+    const float l = clean_logit(raw_logit(row + e));
+    return l > kNegInf ? expf(l - m) * inv * (dv - dot) : 0.0f;
+  };
+  if (vec) {
+    for (int e = 4 * g; e < E; e += 4 * LPT) {
+      const float v0 = value(e), v1 = value(e + 1), v2 = value(e + 2), v3 = value(e + 3);
+      if constexpr (sizeof(LT) == 4) {
+        u32x4 v;
+        v[0] = __float_as_uint(v0);
+        v[1] = __float_as_uint(v1);
+        v[2] = __float_as_uint(v2);
+        v[3] = __float_as_uint(v3);
+        *reinterpret_cast<u32x4*>(out + e) = v;
+      } else {
+        u32x2 v;
+        v[0] = bf16x2_of(v0, v1);
+        v[1] = bf16x2_of(v2, v3);
+        *reinterpret_cast<u32x2*>(out + e) = v;
+      }
+    }
+  } else {
+    for (int e = g; e < E; e += LPT) {
+      if constexpr (sizeof(LT) == 4) out[e] = value(e);
+      else out[e] = bf16_of(value(e));
     }
   }
-  k_route<LPT, NV, LT, false><<<route_blocks(waves), kWave, 0, s>>>(a, waves);
+  lds_sync();
+}
+
+// Tokens up to which one wave takes one token.
+constexpr int64_t kSmallBatch = 2048;
+
+// Blocks of one wave for `waves` wave tasks, in two dimensions: a dimension
+// holds fewer than 2^32 threads.
+dim3 route_grid(int64_t waves) {
+  constexpr int64_t kMaxX = 1 << 22;
+  if (waves <= kMaxX) return dim3(static_cast<unsigned>(waves));
+  return dim3(static_cast<unsigned>(kMaxX), static_cast<unsigned>((waves + kMaxX - 1) / kMaxX));
+}
+
+template <int LPT, int NV, int KEEP, typename LT>
+hipError_t route_k(const RouteArgs& a, hipStream_t s) {
+  const dim3 grid = route_grid((a.T + kWave / LPT - 1) / (kWave / LPT));
+  if (a.bias) k_route<LPT, NV, KEEP, LT, kByScore><<<grid, kWave, 0, s>>>(a);
+  else if constexpr (sizeof(LT) == 2) k_route<LPT, NV, KEEP, LT, kByBf16><<<grid, kWave, 0, s>>>(a);
+  else k_route<LPT, NV, KEEP, LT, kByFp32><<<grid, kWave, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename LT>
 hipError_t route_e(const RouteArgs& a, hipStream_t s) {
-  if (a.E <= 64) return route_k<16, 4, LT>(a, s);
-  if (a.E <= 128) return route_k<16, 8, LT>(a, s);
-  if (a.E <= 256) return route_k<16, 16, LT>(a, s);
-  if (a.E <= 512) return route_k<32, 16, LT>(a, s);
-  return route_k<64, 16, LT>(a, s);
+  if (a.T <= kSmallBatch) {
+    if (a.E <= 256) return route_k<64, 4, 4, LT>(a, s);
+    if (a.E <= 512) return route_k<64, 8, 8, LT>(a, s);
+    return route_k<64, 16, 16, LT>(a, s);
+  }
+  if (a.E <= 64) return route_k<16, 4, 4, LT>(a, s);
+  if (a.E <= 128) return route_k<16, 8, 8, LT>(a, s);
+  if (a.E <= 256) return a.K <= 8 ? route_k<16, 16, 8, LT>(a, s) : route_k<16, 16, 16, LT>(a, s);
+  if (a.E <= 512) return a.K <= 8 ? route_k<32, 16, 8, LT>(a, s) : route_k<32, 16, 16, LT>(a, s);
+  return route_k<64, 16, 16, LT>(a, s);
 }
 
 template <typename LT>
@@ -661,7 +888,7 @@ hipError_t backward_e(const RouteArgs& a, hipStream_t s) {
   auto go = [&](auto kern, int lpt) {
     const int tok = kWave / lpt;
     const int64_t waves = (a.T + tok - 1) / tok;
-    kern<<<route_blocks(waves), kWave, static_cast<size_t>(tok) * cap * sizeof(float), s>>>(a, waves, cap);
+    kern<<<route_grid(waves), kWave, static_cast<size_t>(tok) * cap * sizeof(float), s>>>(a, cap);
     return hipGetLastError();
   };
   if (a.E <= 256) return go(k_route_backward<16, LT>, 16);

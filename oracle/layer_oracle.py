@@ -87,8 +87,8 @@ def weights_rtol(logits, idx):
     step of each logit or difference that forms it (at most four of the
     largest), everything after (exponentials, a sum of up to 1024 terms over
     16 values a lane and 6 levels, quotient, scale) by at most 64 half steps."""
-    big = np.abs(np.where(np.isfinite(logits), logits, 0.0)).max() if logits.size else 0.0
-    return (4 * big + 64) * U32
+    big = np.where(np.isfinite(logits), np.abs(logits), 0.0).max(axis=1, initial=0.0, keepdims=True)
+    return (4 * big + 64) * U32  # per token
 
 
 def route_backward(gw, logits, idx, score="softmax", renorm=False, scale=1.0):
