@@ -72,12 +72,17 @@ struct LoraGeom {
   int64_t rows;       // expert-major rows at most, padding included
   int row_tiles;      // 16-row sub-tiles per row tile: 1, 2 or 4
   int64_t max_tiles;  // row tiles at most
+  int expand_shift;    // log2 of the rows of a tile of the result
+  int64_t max_expand;  // such tiles at most
   int split_x;        // splits of the contraction over H (u = A x)
   int split_g;        // splits of the contraction over N (v = B^T g; backward)
   int chunk_shift;    // log2 of the rows of a weight-gradient chunk
   int64_t max_chunks;  // weight-gradient chunks at most
   int64_t slots;       // partial gradients of experts with several chunks, at most
-  size_t u_bytes, v_bytes, slot_bytes;  // workspace parts, multiples of 16
+  int chunk_waves;     // waves per block of the weight gradients
+  // workspace parts, multiples of 16
+  size_t tile_bytes, expand_bytes, chunk_bytes, u_bytes, v_bytes, slot_bytes;
+  size_t bytes() const { return tile_bytes + expand_bytes + chunk_bytes + u_bytes + v_bytes + slot_bytes; }
 };
 LoraGeom lora_geom(int64_t rows, int E, int H, int N, int R, bool backward);
 
@@ -103,7 +108,10 @@ struct LoraArgs {
   int64_t ldgo;
   uint16_t* ga;  // [E, R, H]
   uint16_t* gb;  // [E, N, R]
-  float* u;      // workspace: split_x partial sums of [rows, R]
+  int32_t* tiles;         // workspace: 4 words per row tile,
+  int32_t* expand_tiles;  // tile of the result
+  int32_t* chunks;        // and weight-gradient chunk
+  float* u;      // split_x partial sums of [rows, R]
   float* v;      // split_g partial sums of [rows, R]
   float* slots;  // partial gradients
   int32_t* status;

@@ -121,6 +121,21 @@ int lora_args(const ep_problem_t* p, const ep_layout_t* L, const ep_lora_weights
   return EP_OK;
 }
 
+void set_workspace(ep::LoraArgs* a, const ep::LoraGeom& g, void* workspace) {
+  char* ws = static_cast<char*>(workspace);
+  auto part = [&](size_t bytes) {
+    char* at = ws;
+    ws += bytes;
+    return at;
+  };
+  a->tiles = reinterpret_cast<int32_t*>(part(g.tile_bytes));
+  a->expand_tiles = reinterpret_cast<int32_t*>(part(g.expand_bytes));
+  a->chunks = reinterpret_cast<int32_t*>(part(g.chunk_bytes));
+  a->u = reinterpret_cast<float*>(part(g.u_bytes));
+  a->v = reinterpret_cast<float*>(part(g.v_bytes));
+  a->slots = reinterpret_cast<float*>(part(g.slot_bytes));
+}
+
 // A matrix of rows: stride (0 = width), alignment.
 int check_rows(const void* p, int64_t stride, int32_t width, int64_t* ld) {
   *ld = stride == 0 ? width : stride;
@@ -225,8 +240,7 @@ int ep_combine_backward(const ep_problem_t* p, const ep_layout_t* L, const float
 size_t ep_lora_workspace_bytes(const ep_problem_t* p, const ep_lora_weights_t* w, int32_t backward) {
   if (check_lora(p, w) != EP_OK) return 0;
   const ep::LoraGeom g = geom_of(p, w, backward != 0);
-  const size_t n = g.u_bytes + g.v_bytes + g.slot_bytes;
-  return n > 0 ? n : 16;  // T = 0 needs none; 0 means refused
+  return g.bytes() > 0 ? g.bytes() : 16;  // T = 0 needs none; 0 means refused
 }
 
 int ep_lora(const ep_problem_t* p, const ep_layout_t* L, const ep_lora_weights_t* w, const void* x,
@@ -251,11 +265,11 @@ int ep_lora(const ep_problem_t* p, const ep_layout_t* L, const ep_lora_weights_t
       rows_overlap(ro, {base, orows, 2LL * a.N, 2 * a.ldbase}))
     return EP_EINVAL;
   if (!workspace || !aligned(workspace, 16)) return EP_EINVAL;
-  if (workspace_bytes < g.u_bytes) return EP_EWORKSPACE;
+  if (workspace_bytes < g.bytes()) return EP_EWORKSPACE;
   a.x = static_cast<const uint16_t*>(x);
   a.base = static_cast<const uint16_t*>(base);
   a.out = static_cast<uint16_t*>(out);
-  a.u = static_cast<float*>(workspace);
+  set_workspace(&a, g, workspace);
   return ep::launch_lora(a, g, stream) == hipSuccess ? EP_OK : EP_EHIP;
 }
 
@@ -302,17 +316,14 @@ int ep_lora_backward(const ep_problem_t* p, const ep_layout_t* L, const ep_lora_
       if (rows_overlap(outs[i], rb)) return EP_EINVAL;
   }
   if (!workspace || !aligned(workspace, 16)) return EP_EINVAL;
-  if (workspace_bytes < g.u_bytes + g.v_bytes + g.slot_bytes) return EP_EWORKSPACE;
+  if (workspace_bytes < g.bytes()) return EP_EWORKSPACE;
   a.x = static_cast<const uint16_t*>(x);
   a.go = static_cast<const uint16_t*>(grad_out);
   a.base = static_cast<const uint16_t*>(grad_base);
   a.out = static_cast<uint16_t*>(grad_x);
   a.ga = static_cast<uint16_t*>(grad_a);
   a.gb = static_cast<uint16_t*>(grad_b);
-  char* ws = static_cast<char*>(workspace);
-  a.u = reinterpret_cast<float*>(ws);
-  a.v = reinterpret_cast<float*>(ws + g.u_bytes);
-  a.slots = reinterpret_cast<float*>(ws + g.u_bytes + g.v_bytes);
+  set_workspace(&a, g, workspace);
   return ep::launch_lora_backward(a, g, stream) == hipSuccess ? EP_OK : EP_EHIP;
 }
 

@@ -18,9 +18,15 @@
 //
 // A matrix whose contraction index is not contiguous in memory is transposed
 // in registers: a lane loads 8 rows of 8 columns and forms, with 32 byte
-// permutes, the 8 operands that hold one column each; operand row rho of
-// product m then stands for column 8 perm(rho) + m.  That also leaves each
-// lane with 8 neighbouring columns of the result.
+// permutes, the 8 operands that hold one column each; operand column l of
+// product c then stands for column 8 l + c.  That also leaves each lane with 8
+// neighbouring columns of the result, and 16 lanes with 256 contiguous bytes.
+//
+// Loads and stores keep neighbouring lanes on neighbouring 16 bytes: a load
+// whose neighbouring lanes lie in different rows costs the L1 one access per
+// lane instead of one per 64 bytes, and measured 1.5 to 2 times slower.
+#include <type_traits>
+
 #include "ep_layer.h"
 
 namespace ep {
@@ -28,8 +34,8 @@ namespace ep {
 namespace {
 
 constexpr int kCols = 128;  // columns of one wave
-constexpr int kRowsStaged = 64;  // rows of u or v staged at a time by the weight gradients
-constexpr int kRowPitch = kRowsStaged + 8;
+constexpr int kXcds = 8;
+constexpr int kMaxSplits = 4;  // splits of a contraction over blocks
 
 __device__ __forceinline__ f32x4_t mfma(u32x4 a, u32x4 b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
@@ -37,6 +43,13 @@ __device__ __forceinline__ f32x4_t mfma(u32x4 a, u32x4 b, f32x4_t c) {
 }
 
 __device__ __forceinline__ u32x4 load16(const uint16_t* p) { return *reinterpret_cast<const u32x4*>(p); }
+
+// LDS that one wave alone uses is accessed in order: only the compiler has to
+// keep the order.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
 // f as bf16 parts hi + lo.  Where hi is infinite lo is 0, not inf - inf.
 __device__ __forceinline__ void split(float f, uint16_t& hi, uint16_t& lo) {
@@ -65,62 +78,88 @@ __device__ __forceinline__ void columns(const u32x4 (&v)[8], u32x4 (&c)[8]) {
   c[7] = column<7>(v);
 }
 
-// Block of 8 columns that operand row rho stands for.  Result rows 4 q + i of
-// quarter q then are blocks 4 i + q: the four quarters' stores of one i are
-// neighbours.
-__device__ __forceinline__ int perm(int rho) { return (rho & 3) * 4 + (rho >> 2); }
-
-// Tile `tile` of the experts' rows cut into tiles of 2^shift rows, experts in
-// order.  Every lane of the wave calls it with the same arguments.
+// Tile `index` of the experts' rows, cut into tiles of 2^shift rows in expert
+// order.  BY_XCD: blocks go round-robin over the 8 XCDs, so index b stands for
+// tile (b % 8) * ceil(tiles / 8) + b / 8, and neighbouring tiles, which share an
+// expert's matrix, meet in one L2.  Every lane calls it with the same arguments.
 struct Tile {
   int e;      // expert, -1: no such tile
-  int im;     // tile within the expert
-  int count;  // the expert's rows
-  int slot;   // tiles of experts with several tiles, before this expert
+  int row0;   // first row
+  int nrows;  // rows of the tile
+  int slot;   // where an expert of several tiles keeps this tile's partial
+              // result: the number of such experts' tiles before; -1 for an expert of one tile
 };
-__device__ __forceinline__ Tile find_tile(const int32_t* counts, int E, int shift, int tile) {
+__device__ __forceinline__ int wave_inclusive_scan(int v) {
+  // within rows of 16 lanes, then row 0's total to row 1 and row 2's to row 3,
+  // then the lower half's to the upper
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);  // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);  // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);  // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31
+  return v;
+}
+template <bool BY_XCD>
+__device__ __forceinline__ Tile find_tile(const int32_t* counts, const int32_t* offsets, int E, int shift,
+                                          int index) {
   const int lane = threadIdx.x & (kWave - 1);
-  const int per = (E + kWave - 1) / kWave;  // at most 16
-  int c[16];
-  int sum = 0, many = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  const int per = (E + kWave - 1) / kWave;  // experts per lane, at most 16
+  auto tiles_of = [&](int c) { return (c + (1 << shift) - 1) >> shift; };
+  int count = 0, sum = 0, many = 0;
+  for (int i = 0; i < per; ++i) {
     const int e = lane * per + i;
-    c[i] = i < per && e < E ? counts[e] : 0;
-    const int n = (c[i] + (1 << shift) - 1) >> shift;
+    count = e < E ? counts[e] : 0;
+    const int n = tiles_of(count);
     sum += n;
     many += n > 1 ? n : 0;
   }
-  int incl = sum, incl_many = many;
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const int a = __shfl_up(incl, off, kWave);
-    const int b = __shfl_up(incl_many, off, kWave);
-    if (lane >= off) {
-      incl += a;
-      incl_many += b;
-    }
+  int incl = wave_inclusive_scan(sum), incl_many = wave_inclusive_scan(many);
+  Tile t = {-1, 0, 0, -1};
+  int tile = index;
+  if (BY_XCD) {
+    const int per_xcd = (readlane(incl, kWave - 1) + kXcds - 1) / kXcds;
+    if (index / kXcds >= per_xcd) return t;
+    tile = (index % kXcds) * per_xcd + index / kXcds;
   }
-  const uint64_t after = ballot(incl > tile);
-  Tile t = {-1, 0, 0, 0};
+  uint64_t after = ballot(incl > tile);
   if (after == 0) return t;
-  const int L = static_cast<int>(__builtin_ctzll(after));
+  int L = static_cast<int>(__builtin_ctzll(after));
   int left = tile - readlane(incl - sum, L);
   int slot = readlane(incl_many - many, L);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int ci = readlane(c[i], L);
-    const int n = (ci + (1 << shift) - 1) >> shift;
-    if (t.e < 0) {
-      if (left < n) {
-        t = {L * per + i, left, ci, slot};
-      } else {
-        left -= n;
-        slot += n > 1 ? n : 0;
-      }
-    }
+  int e = L;
+  if (per > 1) {  // the expert among the lane's
+    const int first = L * per;
+    count = lane < per && first + lane < E ? counts[first + lane] : 0;
+    const int n = tiles_of(count);
+    incl = wave_inclusive_scan(n);
+    incl_many = wave_inclusive_scan(n > 1 ? n : 0);
+    after = ballot(incl > left);
+    L = static_cast<int>(__builtin_ctzll(after));
+    slot += readlane(incl_many - (n > 1 ? n : 0), L);
+    left -= readlane(incl - n, L);
+    e = first + L;
   }
+  count = readlane(count, L);
+  t.e = e;
+  t.row0 = offsets[e] + (left << shift);
+  t.nrows = min(1 << shift, count - (left << shift));
+  t.slot = count > (1 << shift) ? slot + left : -1;
   return t;
+}
+
+// A tile as the first kernel left it in the workspace for the later ones.
+__device__ __forceinline__ Tile stored_tile(const int32_t* tiles, int block) {
+  const int32_t* p = tiles + 4 * static_cast<int64_t>(block);
+  return {__builtin_amdgcn_readfirstlane(p[0]), __builtin_amdgcn_readfirstlane(p[1]),
+          __builtin_amdgcn_readfirstlane(p[2]), __builtin_amdgcn_readfirstlane(p[3])};
+}
+__device__ __forceinline__ void store_tile(int32_t* tiles, int block, const Tile& t) {
+  int32_t* p = tiles + 4 * static_cast<int64_t>(block);
+  p[0] = t.e;
+  p[1] = t.row0;
+  p[2] = t.nrows;
+  p[3] = t.slot;
 }
 
 // ------------------------------------------------------------------- shrink
@@ -133,35 +172,78 @@ struct ShrinkArgs {
   float* part;     // [S, rows, R]
   int64_t stride;  // rows * R
   int S;
+  int32_t* tiles;  // written by the blocks of split 0, or (known) read
+  bool known;
+  // the same for the kernels to come, written by two waves of these blocks
+  int32_t* expand_tiles;
+  int num_expand, expand_shift;
+  int32_t* chunks;  // num_chunks == 0: none
+  int num_chunks, chunk_shift;
   const int32_t* counts;
   const int32_t* offsets;
   int32_t* status;
   uint32_t generation;
 };
 
+constexpr int kStageBlocks = 256;  // 8 x 8 blocks of a k-major matrix staged at a time
+
 // Block: one row tile (16 MT rows) and one split of the contraction, whose
-// 64-wide pieces the 4 waves take in turn.
-template <int RT, int MT, bool KMAJOR>
-__global__ __launch_bounds__(kBlock) void k_lora_shrink(ShrinkArgs a) {
+// 64-wide pieces the NW waves take in turn, the next piece's loads in flight
+// while one is multiplied.  The waves' sums are added in wave order.  Four
+// waves a block: several blocks share a CU, and one's start and end hide
+// behind another's loads.
+template <int RT, int MT, int NW, bool KMAJOR>
+__global__ __launch_bounds__(NW* kWave) void k_lora_shrink(ShrinkArgs a) {
   constexpr int kShift = MT == 1 ? 4 : MT == 2 ? 5 : 6;
   constexpr int kPitch = RT * 16 + 4;
-  __shared__ float red[MT * 16 * kPitch];
+  // k-major: 32 KiB of the matrix, transposed: RT * 16 rows of kStage (and 8,
+  // so that rows start on different banks)
+  constexpr int kStage = kStageBlocks * 64 / (RT * 16);
+  constexpr int kRed = MT * 16 * kPitch;  // one wave's sums
+  constexpr int kRedBytes = NW * kRed * 4;
+  constexpr int kXBytes = NW * (KMAJOR ? MT : MT + RT) * 2048;
+  constexpr int kWBytes = KMAJOR ? RT * 16 * (kStage + 8) * 2 : 0;
+  __shared__ __align__(16) char s_mem[kRedBytes > kWBytes + kXBytes ? kRedBytes : kWBytes + kXBytes];
   if (!layout_current(a.status, a.generation)) return;
-  const Tile t = find_tile(a.counts, a.E, kShift, static_cast<int>(blockIdx.x));
+  const int block = static_cast<int>(blockIdx.x);
+  const Tile t = a.known ? stored_tile(a.tiles, block) : find_tile<true>(a.counts, a.offsets, a.E, kShift, block);
+  if (!a.known && blockIdx.y == 0) {
+    if (threadIdx.x == 0) store_tile(a.tiles, block, t);
+    const int w = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+    auto table = [&](int32_t* out, int n, int shift) {
+      for (int b = block; b < n; b += static_cast<int>(gridDim.x)) {
+        const Tile c = find_tile<false>(a.counts, a.offsets, a.E, shift, b);
+        if ((threadIdx.x & (kWave - 1)) == 0) store_tile(out, b, c);
+      }
+    };
+    if (w == 1) table(a.expand_tiles, a.num_expand, a.expand_shift);
+    if (w == 2) table(a.chunks, a.num_chunks, a.chunk_shift);
+  }
   if (t.e < 0) return;  // the whole block
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const int l16 = lane & 15, q = lane >> 4;
-  const int row0 = a.offsets[t.e] + (t.im << kShift);
-  const int nrows = min(16 * MT, t.count - (t.im << kShift));
 
-  const uint16_t* xr[MT];
+  // A wave's 64-wide piece of its rows passes through LDS: loaded 8 rows of a
+  // whole 128-byte line per instruction, read as operands.  16-byte unit u of
+  // row r lies at r * 8 + (u ^ ((r >> 1) & 7)), which keeps the reads of 16 rows
+  // at one u on distinct banks.
+  const int l8 = lane >> 3, unit = lane & 7;
+  const uint16_t* xr[2 * MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int r = row0 + min(m * 16 + l16, nrows - 1);  // rows past the tile repeat its last
-    xr[m] = a.in + static_cast<int64_t>(a.map ? a.map[r] : r) * a.ld;
+  for (int n = 0; n < 2 * MT; ++n) {
+    const int r = t.row0 + min(n * 8 + l8, t.nrows - 1);  // rows past the tile repeat its last
+    xr[n] = a.in + static_cast<int64_t>(a.map ? a.map[r] : r) * a.ld + unit * 8;
   }
   const uint16_t* w = a.w + static_cast<int64_t>(t.e) * a.R * a.C;
+  u32x4* s_x = reinterpret_cast<u32x4*>(s_mem + kWBytes) + wave * (KMAJOR ? MT : MT + RT) * 128;
+  u32x4* s_wt = s_x + MT * 128;
+  auto put = [&](u32x4* to, int n, u32x4 v) __attribute__((always_inline)) {
+    to[(n * 8 + l8) * 8 + (unit ^ ((n * 4 + (lane >> 4)) & 7))] = v;
+  };
+  auto get = [&](const u32x4* from, int m, int h) __attribute__((always_inline)) {
+    return from[(m * 16 + l16) * 8 + ((h * 4 + q) ^ ((l16 >> 1) & 7))];
+  };
   f32x4_t acc[MT][RT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -172,61 +254,129 @@ __global__ __launch_bounds__(kBlock) void k_lora_shrink(ShrinkArgs a) {
   const int s = static_cast<int>(blockIdx.y);
   const int p0 = static_cast<int>(static_cast<int64_t>(pieces) * s / a.S);
   const int p1 = static_cast<int>(static_cast<int64_t>(pieces) * (s + 1) / a.S);
-  for (int p = p0 + wave; p < p1; p += kWavesPerBlock) {
+
+  // Elements past C (a multiple of 8) are zeros, in both operands: loaded from
+  // the last 8, replaced when they are put into LDS.
+  auto place = [&](int p) __attribute__((always_inline)) { return min(p * 64, a.C - 8 - unit * 8); };
+  auto past = [&](int p) __attribute__((always_inline)) { return p * 64 + unit * 8 >= a.C; };
+  auto load_x = [&](int p, u32x4 (&x)[2 * MT]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = p * 64 + h * 32 + q * 8;
-      const bool ok = k < a.C;  // C is a multiple of 8
-      u32x4 xv[MT], wv[RT];
+    for (int n = 0; n < 2 * MT; ++n) x[n] = load16(xr[n] + place(p));
+  };
+  auto put_x = [&](int p, u32x4 (&x)[2 * MT]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        xv[m] = u32x4{0u, 0u, 0u, 0u};
-        if (ok) xv[m] = load16(xr[m] + k);
+    for (int n = 0; n < 2 * MT; ++n) put(s_x, n, past(p) ? u32x4{0u, 0u, 0u, 0u} : x[n]);
+  };
+  if constexpr (!KMAJOR) {
+    const uint16_t* wr[2 * RT];
+#pragma unroll
+    for (int n = 0; n < 2 * RT; ++n)  // rows past R repeat the last, and are dropped
+      wr[n] = w + static_cast<int64_t>(min(n * 8 + l8, a.R - 1)) * a.C + unit * 8;
+    auto load_w = [&](int p, u32x4 (&v)[2 * RT]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int n = 0; n < 2 * RT; ++n) v[n] = load16(wr[n] + place(p));
+    };
+    u32x4 x[2 * MT], v[2 * RT];
+    int p = p0 + wave;
+    if (p < p1) {
+      load_x(p, x);
+      load_w(p, v);
+    }
+    while (p < p1) {
+      wave_lds_sync();  // the last piece's operands are read
+      put_x(p, x);
+#pragma unroll
+      for (int n = 0; n < 2 * RT; ++n) put(s_wt, n, past(p) ? u32x4{0u, 0u, 0u, 0u} : v[n]);
+      wave_lds_sync();
+      p += NW;
+      if (p < p1) {
+        load_x(p, x);
+        load_w(p, v);
       }
 #pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        const int jr = min(j * 16 + l16, a.R - 1);  // columns past R repeat the last, and are dropped
-        wv[j] = u32x4{0u, 0u, 0u, 0u};
-        if (ok) {
-          if (KMAJOR) {
+      for (int h = 0; h < 2; ++h) {
+        u32x4 wv[RT];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint16_t* wp = w + static_cast<int64_t>(k + 2 * i) * a.R + jr;
-              wv[j][i] = static_cast<uint32_t>(wp[0]) | (static_cast<uint32_t>(wp[a.R]) << 16);
-            }
-          } else {
-            wv[j] = load16(w + static_cast<int64_t>(jr) * a.C + k);
+        for (int j = 0; j < RT; ++j) wv[j] = get(s_wt, j, h);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const u32x4 xv = get(s_x, m, h);
+#pragma unroll
+          for (int j = 0; j < RT; ++j) acc[m][j] = mfma(wv[j], xv, acc[m][j]);
+        }
+      }
+    }
+  } else {
+    uint16_t* s_w = reinterpret_cast<uint16_t*>(s_mem);
+    constexpr int kWPitch = kStage + 8;
+    const int k_end = min(p1 * 64, a.C);
+    for (int k0 = p0 * 64; k0 < k_end; k0 += kStage) {
+      u32x4 x[2 * MT];
+      int k = k0 + wave * 64;
+      const int q1 = min(k0 + kStage, k_end);
+      if (k < q1) load_x(k / 64, x);
+      // 8 x 8 blocks (8 k, 8 of R) transposed in registers, k contiguous in LDS
+      if (k0 > p0 * 64) __syncthreads();
+      for (int b = threadIdx.x; b < kStageBlocks; b += NW * kWave) {
+        const int jb = b % (RT * 2), kb = b / (RT * 2);
+        const int kk = k0 + kb * 8;
+        u32x4 v[8], c[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] = u32x4{0u, 0u, 0u, 0u};
+          if (kk < k_end && jb * 8 < a.R) v[i] = load16(w + static_cast<int64_t>(kk + i) * a.R + jb * 8);
+        }
+        columns(v, c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<u32x4*>(s_w + (jb * 8 + i) * kWPitch + kb * 8) = c[i];
+      }
+      __syncthreads();
+      for (; k < q1; k += NW * 64) {
+        wave_lds_sync();
+        put_x(k / 64, x);
+        wave_lds_sync();
+        if (k + NW * 64 < q1) load_x(k / 64 + NW, x);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          u32x4 v[RT];
+#pragma unroll
+          for (int j = 0; j < RT; ++j)
+            v[j] = *reinterpret_cast<const u32x4*>(s_w + (j * 16 + l16) * kWPitch + k - k0 + h * 32 + q * 8);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const u32x4 xv = get(s_x, m, h);
+#pragma unroll
+            for (int j = 0; j < RT; ++j) acc[m][j] = mfma(v[j], xv, acc[m][j]);
           }
         }
       }
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < RT; ++j) acc[m][j] = mfma(wv[j], xv[m], acc[m][j]);
     }
   }
-  // the waves' sums, added in wave order
-  for (int n = 0; n < kWavesPerBlock; ++n) {
-    if (wave == n) {
+  __syncthreads();  // the operands' LDS is reused
+  float* red = reinterpret_cast<float*>(s_mem);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int j = 0; j < RT; ++j) {
-          f32x4_t* d = reinterpret_cast<f32x4_t*>(red + (m * 16 + l16) * kPitch + j * 16 + q * 4);
-          *d = n == 0 ? acc[m][j] : *d + acc[m][j];
-        }
-    }
-    __syncthreads();
+    for (int j = 0; j < RT; ++j)
+      *reinterpret_cast<f32x4_t*>(red + wave * kRed + (m * 16 + l16) * kPitch + j * 16 + q * 4) = acc[m][j];
+  __syncthreads();
+  float* out = a.part + s * a.stride + static_cast<int64_t>(t.row0) * a.R;
+  const int quads = a.R / 4;
+  for (int i = threadIdx.x; i < t.nrows * quads; i += NW * kWave) {
+    const float* p = red + (i / quads) * kPitch + i % quads * 4;
+    f32x4_t f = *reinterpret_cast<const f32x4_t*>(p);
+#pragma unroll
+    for (int n = 1; n < NW; ++n) f += *reinterpret_cast<const f32x4_t*>(p + n * kRed);
+    *reinterpret_cast<f32x4_t*>(out + 4 * i) = f;
   }
-  float* out = a.part + s * a.stride + static_cast<int64_t>(row0) * a.R;
-  for (int i = threadIdx.x; i < nrows * a.R; i += kBlock) out[i] = red[(i / a.R) * kPitch + i % a.R];
 }
 
 // ------------------------------------------------------------------- expand
 struct ExpandArgs {
   const float* part;  // [S, rows, R]
   int64_t stride;
-  int S;
+  int S;  // 1, 2 or 4
   const uint16_t* w;  // [E, N, R], or (JMAJOR) [E, R, N]
   const float* scales;
   const uint16_t* base;
@@ -236,9 +386,8 @@ struct ExpandArgs {
   const int32_t* map;
   const int32_t* slot;
   int64_t T;
-  int N, R, E;
-  const int32_t* counts;
-  const int32_t* offsets;
+  int N, R;
+  const int32_t* tiles;
   int32_t* status;
   uint32_t generation;
 };
@@ -246,7 +395,6 @@ struct ExpandArgs {
 // Rows of out that belong to no selection (token rows only): base's row, or
 // zeros.  32 tokens per block.
 __device__ __forceinline__ void copy_unselected(const ExpandArgs& a, int64_t t0, int wave, int lane) {
-  if (a.base == a.out) return;
   for (int i = 0; i < 8; ++i) {
     const int64_t t = t0 + wave * 8 + i;
     if (t >= a.T || a.slot[t] >= 0) continue;
@@ -258,119 +406,205 @@ __device__ __forceinline__ void copy_unselected(const ExpandArgs& a, int64_t t0,
   }
 }
 
-// Block: one row tile by 512 columns.  PACK: R <= 16, the high parts in the
-// first half of one contraction step and the low parts in the second.
-template <int KS, int MT, bool PACK, bool JMAJOR>
-__global__ __launch_bounds__(kBlock) void k_lora_expand(ExpandArgs a) {
-  constexpr int kShift = MT == 1 ? 4 : MT == 2 ? 5 : 6;
+// Quads (4 neighbouring elements) of u or v, the S splits added in order,
+// passed on one by one: put(i, quad) for every i of the block's threads below
+// `count`, where at(i) is the quad's place in a split, or null for zeros.  Four
+// quads' loads are in flight together.
+template <int S, typename At, typename Put>
+__device__ __forceinline__ void joined_quads(int count, int64_t stride, At at, Put put) {
+  constexpr int kBatch = 4;
+  const int nt = static_cast<int>(blockDim.x);
+  for (int i0 = threadIdx.x; i0 < count; i0 += kBatch * nt) {
+    f32x4_t f[kBatch][S];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const float* p = i0 + b * nt < count ? at(i0 + b * nt) : nullptr;
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        f[b][s] = f32x4_t{};
+        if (p) f[b][s] = *reinterpret_cast<const f32x4_t*>(p + s * stride);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (i0 + b * nt >= count) continue;
+      f32x4_t sum = f[b][0];
+#pragma unroll
+      for (int s = 1; s < S; ++s) sum += f[b][s];
+      put(i0 + b * nt, sum);
+    }
+  }
+}
+template <typename At, typename Put>
+__device__ __forceinline__ void joined_quads(int S, int count, int64_t stride, At at, Put put) {
+  if (S == 1) joined_quads<1>(count, stride, at, put);
+  else if (S == 2) joined_quads<2>(count, stride, at, put);
+  else joined_quads<4>(count, stride, at, put);
+}
+__device__ __forceinline__ void split4(f32x4_t f, u32x2& hi, u32x2& lo) {
+  uint16_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split(f[i], h[i], l[i]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    hi[i] = h[2 * i] | (static_cast<uint32_t>(h[2 * i + 1]) << 16);
+    lo[i] = l[2 * i] | (static_cast<uint32_t>(l[2 * i + 1]) << 16);
+  }
+}
+
+// Rows of a result tile at most, as much of u as LDS holds comfortably.
+__host__ __device__ constexpr int expand_rows(int KS) { return KS <= 2 ? 128 : 64; }
+
+// Block: one tile of rows by 512 columns.  u's rows are put into LDS, as their
+// two bf16 parts; a wave holds its 128 columns of the matrix in registers and
+// takes the tile's rows 16 at a time, the next 32 rows' base in flight.  The
+// loop over whole groups has no condition inside: memory operations complete in
+// order, and with a load or store that may be skipped the compiler waits for
+// all of them instead of counting.  PACK: R <= 16, the high parts in the first
+// half of one contraction step and the low parts in the second.
+template <int KS, bool PACK, bool JMAJOR>
+__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(KS == 1 ? 3 : 2))) void k_lora_expand(
+    ExpandArgs a) {
   if (!layout_current(a.status, a.generation)) return;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+  constexpr int kPitch = KS * 32 + 8;
+  constexpr int kStaged = expand_rows(KS);
+  __shared__ __align__(16) uint16_t s_u[PACK ? 1 : 2][kStaged * kPitch];
+  __shared__ int s_row[kStaged];
   const int ncb = (a.N + 4 * kCols - 1) / (4 * kCols);
-  if (static_cast<int>(blockIdx.y) == ncb) {  // the layer of rows of no selection
-    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * 32; t0 < a.T; t0 += static_cast<int64_t>(gridDim.x) * 32)
+  if (static_cast<int>(blockIdx.x) == ncb) {  // the column of rows of no selection
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * 32; t0 < a.T; t0 += static_cast<int64_t>(gridDim.y) * 32)
       copy_unselected(a, t0, wave, lane);
     return;
   }
-  const Tile t = find_tile(a.counts, a.E, kShift, static_cast<int>(blockIdx.x));
+  const Tile t = stored_tile(a.tiles, static_cast<int>(blockIdx.y));
   if (t.e < 0) return;
-  const int n0 = (static_cast<int>(blockIdx.y) * 4 + wave) * kCols;
-  if (n0 >= a.N) return;
+  const int n0 = (static_cast<int>(blockIdx.x) * 4 + wave) * kCols;
   const int l16 = lane & 15, q = lane >> 4;
-  const int row0 = a.offsets[t.e] + (t.im << kShift);
-  const int nrows = min(16 * MT, t.count - (t.im << kShift));
   const float scale = a.scales ? a.scales[t.e] : 1.0f;
-
-  // operands of the rows: 8 of u's elements as high and low parts
-  u32x4 hi[MT][KS], lo[MT][KS];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int r = row0 + min(m * 16 + l16, nrows - 1);
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const int j = PACK ? (q & 1) * 8 : ks * 32 + q * 8;
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = 0.0f;
-      if (j < a.R) {
-        for (int s = 0; s < a.S; ++s) {
-          const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.part + s * a.stride + static_cast<int64_t>(r) * a.R + j);
-          const f32x4_t p0 = p[0], p1 = p[1];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f[i] += p0[i];
-            f[4 + i] += p1[i];
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint16_t h0, l0, h1, l1;
-        split(f[2 * i], h0, l0);
-        split(f[2 * i + 1], h1, l1);
-        const uint32_t hh = h0 | (static_cast<uint32_t>(h1) << 16);
-        const uint32_t ll = l0 | (static_cast<uint32_t>(l1) << 16);
-        hi[m][ks][i] = PACK && q >= 2 ? ll : hh;
-        lo[m][ks][i] = ll;
-      }
-    }
-  }
-
   const uint16_t* w = a.w + static_cast<int64_t>(t.e) * a.R * a.N;
-  const int blk = n0 + perm(l16) * 8;  // first of this operand row's 8 columns
-  f32x4_t acc[MT][8];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int c = 0; c < 8; ++c) acc[m][c] = f32x4_t{};
+
+  // the rows' places in base and out; rows past the tile repeat its last
+  for (int r = threadIdx.x; r < kStaged; r += kBlock) {
+    const int at = t.row0 + min(r, t.nrows - 1);
+    s_row[r] = a.map ? a.map[at] : at;
+  }
+  // Columns n .. n + 7 of this lane.  Lanes past N work on the last 8 columns
+  // and store nothing; R's elements past R are zeros.
+  const bool whole = n0 + kCols <= a.N;
+  const bool inside = n0 + l16 * 8 < a.N;
+  const int n = inside ? n0 + l16 * 8 : a.N - 8;
+  u32x4 wv[KS][8];
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) {
     const int j = PACK ? (q & 1) * 8 : ks * 32 + q * 8;
-    u32x4 wv[8];
-    const bool ok = j < a.R && blk < a.N;
-    if (JMAJOR) {
-      u32x4 v[8];
+    u32x4 v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = u32x4{0u, 0u, 0u, 0u};
-        if (ok) v[i] = load16(w + static_cast<int64_t>(j + i) * a.N + blk);
-      }
-      columns(v, wv);
+    for (int i = 0; i < 8; ++i) {
+      v[i] = u32x4{0u, 0u, 0u, 0u};
+      if (j < a.R) v[i] = JMAJOR ? load16(w + static_cast<int64_t>(j + i) * a.N + n)
+                                 : load16(w + static_cast<int64_t>(n + i) * a.R + j);
+    }
+    if (JMAJOR) {
+      columns(v, wv[ks]);
     } else {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        wv[c] = u32x4{0u, 0u, 0u, 0u};
-        if (ok) wv[c] = load16(w + static_cast<int64_t>(blk + c) * a.R + j);
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        acc[m][c] = mfma(wv[c], hi[m][ks], acc[m][c]);
-        if (!PACK) acc[m][c] = mfma(wv[c], lo[m][ks], acc[m][c]);
-      }
+      for (int i = 0; i < 8; ++i) wv[ks][i] = v[i];
     }
   }
+  constexpr int kQuads = PACK ? 4 : KS * 8;  // of a row, the ones past R zeros
+  const int groups = (t.nrows + 15) / 16;
+  joined_quads(
+      a.S, groups * 16 * kQuads, a.stride,
+      [&](int i) -> const float* {
+        const int r = i / kQuads, j = i % kQuads * 4;
+        if (r >= t.nrows || j >= a.R) return nullptr;
+        return a.part + static_cast<int64_t>(t.row0 + r) * a.R + j;
+      },
+      [&](int i, f32x4_t f) {
+        const int r = i / kQuads, j = i % kQuads * 4;
+        u32x2 hi, lo;
+        split4(f, hi, lo);
+        *reinterpret_cast<u32x2*>(&s_u[0][r * kPitch + j]) = hi;
+        *reinterpret_cast<u32x2*>(PACK ? &s_u[0][r * kPitch + 16 + j] : &s_u[PACK ? 0 : 1][r * kPitch + j]) = lo;
+      });
+  __syncthreads();
+  if (n0 >= a.N) return;
+
+  // this lane's rows 4 q + i of group m
+  auto rows = [&](int m, int64_t (&row)[4]) __attribute__((always_inline)) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int rl = m * 16 + l16;
-    if (rl >= nrows) continue;
-    const int r = row0 + rl;
-    const int64_t orow = a.map ? a.map[r] : r;
+    for (int i = 0; i < 4; ++i) row[i] = s_row[m * 16 + q * 4 + i];
+  };
+  auto load_base = [&](const int64_t (&row)[4], u32x4 (&b)[4]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = n0 + (i * 4 + q) * 8;
-      if (n >= a.N) continue;
-      u32x4 bv = {0u, 0u, 0u, 0u};
-      if (a.base) bv = load16(a.base + orow * a.ldbase + n);
-      u32x4 o;
+    for (int i = 0; i < 4; ++i) b[i] = load16(a.base + row[i] * a.ldbase + n);
+  };
+  auto result = [&](int m, const u32x4 (&base)[4], u32x4 (&o)[4]) __attribute__((always_inline)) {
+    f32x4_t acc[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] = f32x4_t{};
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int at = (m * 16 + l16) * kPitch + ks * 32 + q * 8;
+#pragma unroll
+      for (int d = 0; d < (PACK ? 1 : 2); ++d) {
+        const u32x4 u = *reinterpret_cast<const u32x4*>(&s_u[d][at]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] = mfma(u, wv[ks][c], acc[c]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        o[c] = bf16x2_of(__builtin_fmaf(scale, acc[m][2 * c][i], bf16_lo(bv[c])),
-                         __builtin_fmaf(scale, acc[m][2 * c + 1][i], bf16_hi(bv[c])));
-      *reinterpret_cast<u32x4*>(a.out + orow * a.ldout + n) = o;
+        o[i][c] = bf16x2_of(__builtin_fmaf(scale, acc[2 * c][i], bf16_lo(base[i][c])),
+                            __builtin_fmaf(scale, acc[2 * c + 1][i], bf16_hi(base[i][c])));
+  };
+  // whole groups, two at a time
+  const int pairs = whole ? t.nrows / 32 : 0;
+  auto whole_groups = [&](auto with_base) __attribute__((always_inline)) {
+    int64_t row[2][4];
+    u32x4 base[2][4] = {};
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      rows(d, row[d]);
+      if (with_base.value) load_base(row[d], base[d]);
     }
+    auto pair = [&](int p) __attribute__((always_inline)) {
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        u32x4 o[4];
+        result(2 * p + d, base[d], o);
+        int64_t next[4];
+        rows(min(2 * p + d + 2, kStaged / 16 - 1), next);  // past the tile: its last row
+        if (with_base.value) load_base(next, base[d]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          *reinterpret_cast<u32x4*>(a.out + row[d][i] * a.ldout + n) = o[i];
+          row[d][i] = next[i];
+        }
+      }
+    };
+    // the first apart: at the loop's head as many operations then are open on
+    // entry as on return
+    pair(0);
+    for (int p = 1; p < pairs; ++p) pair(p);
+  };
+  if (pairs > 0) {
+    if (a.base) whole_groups(std::integral_constant<bool, true>());
+    else whole_groups(std::integral_constant<bool, false>());
+  }
+  for (int m = 2 * pairs; m < groups; ++m) {
+    int64_t row[4];
+    u32x4 base[4] = {}, o[4];
+    rows(m, row);
+    if (a.base) load_base(row, base);
+    result(m, base, o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (inside && m * 16 + q * 4 + i < t.nrows) *reinterpret_cast<u32x4*>(a.out + row[i] * a.ldout + n) = o[i];
   }
 }
 
@@ -382,36 +616,38 @@ struct WeightGradArgs {
   const int32_t* map[2];
   int C[2];            // columns: H, N
   const float* part[2];  // v, u: [S, rows, R]
-  int S[2];
+  int S[2];              // 1, 2 or 4
   int64_t stride;
   uint16_t* out[2];  // dA [E, R, H], dB [E, N, R]
   float* slots;
   int64_t slot_size;  // R * (H + N)
   const float* scales;
   int R, E, shift;
+  const int32_t* chunks;
   const int32_t* counts;
-  const int32_t* offsets;
   int32_t* status;
   uint32_t generation;
 };
 
-// Block: one chunk of an expert's rows, 512 columns of x (or g), 16 JT of the
-// R.  The columns are the row operand for dA, whose rows are R's, and the
-// column operand for dB, whose rows are the columns: each lane ends with
-// neighbouring elements of the result.
-template <int JT, int B>
-__device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile& t, int cb, int jg,
-                                            uint16_t (*s_hi)[kRowPitch], uint16_t (*s_lo)[kRowPitch]) {
+// Rows of u or v that a block holds in LDS at a time: 16 KiB as two bf16 parts.
+__host__ __device__ constexpr int staged_rows(int JT) { return 256 / JT; }
+
+// Block: one chunk of an expert's rows, 128 NW columns of x (or g), 16 JT of the
+// R.  A wave takes 32 rows by 128 columns per step, two steps in flight, loaded
+// without a condition (see k_lora_expand).  A lane ends with R's 4 q + i (i < 4)
+// of each 16 and 8 neighbouring columns.
+template <int JT, int NW, int B>
+__device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile& t, int cb, int jg, uint16_t* s_hi,
+                                            uint16_t* s_lo, int* s_row) {
+  constexpr int kStaged = staged_rows(JT);
+  constexpr int kPitch = kStaged + 8;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const int l16 = lane & 15, q = lane >> 4;
   const int C = a.C[B], R = a.R;
-  const int c0 = (cb * 4 + wave) * kCols;
-  const int col = c0 + perm(l16) * 8;
+  const int c0 = (cb * NW + wave) * kCols;
+  const int col = c0 + l16 * 8;
   const int j0 = jg * JT * 16;
-  const int first = t.im << a.shift;
-  const int row0 = a.offsets[t.e] + first;
-  const int nrows = min(1 << a.shift, t.count - first);
 
   f32x4_t acc[8][JT];
 #pragma unroll
@@ -419,45 +655,57 @@ __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile&
 #pragma unroll
     for (int j = 0; j < JT; ++j) acc[c][j] = f32x4_t{};
 
-  for (int r0 = 0; r0 < nrows; r0 += kRowsStaged) {
-    __syncthreads();  // the rows staged before are used up
-    for (int i = threadIdx.x; i < kRowsStaged * JT * 16; i += kBlock) {
-      const int r = i / (JT * 16), j = i % (JT * 16);
-      float f = 0.0f;
-      if (r0 + r < nrows && j0 + j < R) {
-        const float* p = a.part[B] + static_cast<int64_t>(row0 + r0 + r) * R + j0 + j;
-        for (int s = 0; s < a.S[B]; ++s) f += p[s * a.stride];
-      }
-      uint16_t h, l;
-      split(f, h, l);
-      s_hi[j][r] = h;
-      s_lo[j][r] = l;
-    }
+  // the rows' places; lanes past C work on its last 8 columns and store nothing
+  for (int r = threadIdx.x; r < t.nrows; r += NW * kWave) s_row[r] = a.map[B] ? a.map[B][t.row0 + r] : t.row0 + r;
+  __syncthreads();
+  const uint16_t* in = a.in[B] + min(col, C - 8);
+  auto load_step = [&](int r, u32x4 (&v)[8]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = load16(in + s_row[min(r + q * 8 + i, t.nrows - 1)] * a.ld[B]);
+  };
+  u32x4 v[2][8];
+  load_step(0, v[0]);
+  load_step(32, v[1]);
+  for (int r0 = 0; r0 < t.nrows; r0 += kStaged) {
+    if (r0 > 0) __syncthreads();  // the rows staged before are used up
+    const int staged = min(kStaged, (t.nrows - r0 + 63) / 64 * 64);
+    joined_quads(
+        a.S[B], staged * JT * 4, a.stride,
+        [&](int i) -> const float* {
+          const int r = i / (JT * 4), j = j0 + i % (JT * 4) * 4;
+          if (r0 + r >= t.nrows || j >= R) return nullptr;
+          return a.part[B] + static_cast<int64_t>(t.row0 + r0 + r) * R + j;
+        },
+        [&](int i, f32x4_t f) {
+          const int r = i / (JT * 4), j = i % (JT * 4) * 4;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            uint16_t h, l;
+            split(f[d], h, l);
+            s_hi[(j + d) * kPitch + r] = h;
+            s_lo[(j + d) * kPitch + r] = l;
+          }
+        });
     __syncthreads();
+    for (int r = 0; r < staged; r += 64) {
 #pragma unroll
-    for (int ks = 0; ks < kRowsStaged / 32; ++ks) {
-      const int rq = r0 + ks * 32 + q * 8;
-      u32x4 v[8], cv[8];
+      for (int d = 0; d < 2; ++d) {
+        const int at_row = r0 + r + d * 32;
+        if (at_row + 32 > t.nrows) {  // rows past the chunk are zeros in both operands
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = u32x4{0u, 0u, 0u, 0u};
-        if (rq + i < nrows && col < C) {
-          const int r = row0 + rq + i;
-          const int64_t xr = a.map[B] ? a.map[B][r] : r;
-          v[i] = load16(a.in[B] + xr * a.ld[B] + col);
+          for (int i = 0; i < 8; ++i)
+            if (at_row + q * 8 + i >= t.nrows) v[d][i] = u32x4{0u, 0u, 0u, 0u};
         }
-      }
-      columns(v, cv);
+        u32x4 cv[8];
+        columns(v[d], cv);
+        load_step(at_row + 64, v[d]);
 #pragma unroll
-      for (int j = 0; j < JT; ++j) {
-        const u32x4 h = *reinterpret_cast<const u32x4*>(&s_hi[j * 16 + l16][ks * 32 + q * 8]);
-        const u32x4 l = *reinterpret_cast<const u32x4*>(&s_lo[j * 16 + l16][ks * 32 + q * 8]);
+        for (int j = 0; j < JT; ++j) {
+          const int at = (j * 16 + l16) * kPitch + r + d * 32 + q * 8;
+          const u32x4 h = *reinterpret_cast<const u32x4*>(s_hi + at);
+          const u32x4 l = *reinterpret_cast<const u32x4*>(s_lo + at);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if (B == 0) {
-            acc[c][j] = mfma(cv[c], h, acc[c][j]);
-            acc[c][j] = mfma(cv[c], l, acc[c][j]);
-          } else {
+          for (int c = 0; c < 8; ++c) {
             acc[c][j] = mfma(h, cv[c], acc[c][j]);
             acc[c][j] = mfma(l, cv[c], acc[c][j]);
           }
@@ -466,23 +714,20 @@ __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile&
     }
   }
 
-  const bool whole = t.count <= (1 << a.shift);
+  const bool whole = t.slot < 0;
   const float scale = whole && a.scales ? a.scales[t.e] : 1.0f;
   uint16_t* out = a.out[B] + static_cast<int64_t>(t.e) * R * C;
   float* slot = whole ? nullptr
-                      : a.slots + static_cast<int64_t>(t.slot + t.im) * a.slot_size +
+                      : a.slots + static_cast<int64_t>(t.slot) * a.slot_size +
                             (B == 0 ? 0 : static_cast<int64_t>(R) * a.C[0]);
 #pragma unroll
   for (int j = 0; j < JT; ++j) {
+    const int jr = j0 + j * 16 + q * 4;
+    if (jr >= R || col >= C) continue;
     if (B == 0) {
-      // rows 4 q + i: columns c0 + (4 i + q) 8 + c; column l16: row j of dA
-      const int jr = j0 + j * 16 + l16;
-      if (jr >= R) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int n = c0 + (i * 4 + q) * 8;
-        if (n >= C) continue;
-        const int64_t at = static_cast<int64_t>(jr) * C + n;
+        const int64_t at = static_cast<int64_t>(jr + i) * C + col;
         if (whole) {
           u32x4 o;
 #pragma unroll
@@ -499,9 +744,6 @@ __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile&
         }
       }
     } else {
-      // rows 4 q + i: R's j0 + 16 j + 4 q + i; column l16: columns col + c
-      const int jr = j0 + j * 16 + q * 4;
-      if (jr >= R || col >= C) continue;
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         const int64_t at = static_cast<int64_t>(col + c) * R + jr;
@@ -518,50 +760,68 @@ __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile&
   }
 }
 
-template <int JT>
-__global__ __launch_bounds__(kBlock) void k_lora_weight_grad(WeightGradArgs a) {
-  __shared__ __align__(16) uint16_t s_hi[JT * 16][kRowPitch];
-  __shared__ __align__(16) uint16_t s_lo[JT * 16][kRowPitch];
+template <int JT, int NW>
+__global__ __launch_bounds__(NW* kWave) void k_lora_weight_grad(WeightGradArgs a) {
+  constexpr int kElems = JT * 16 * (staged_rows(JT) + 8);
+  __shared__ __align__(16) uint16_t s_hi[kElems];
+  __shared__ __align__(16) uint16_t s_lo[kElems];
+  extern __shared__ int s_row[];  // a chunk's rows
   if (!layout_current(a.status, a.generation)) return;
-  const Tile t = find_tile(a.counts, a.E, a.shift, static_cast<int>(blockIdx.x));
+  const Tile t = stored_tile(a.chunks, static_cast<int>(blockIdx.y));
   if (t.e < 0) return;
-  const int nca = (a.C[0] + 4 * kCols - 1) / (4 * kCols);
-  const int cb = static_cast<int>(blockIdx.y);
-  if (cb < nca) weight_grad<JT, 0>(a, t, cb, static_cast<int>(blockIdx.z), s_hi, s_lo);
-  else weight_grad<JT, 1>(a, t, cb - nca, static_cast<int>(blockIdx.z), s_hi, s_lo);
+  const int nca = (a.C[0] + NW * kCols - 1) / (NW * kCols);
+  const int cb = static_cast<int>(blockIdx.x);
+  if (cb < nca) weight_grad<JT, NW, 0>(a, t, cb, static_cast<int>(blockIdx.z), s_hi, s_lo, s_row);
+  else weight_grad<JT, NW, 1>(a, t, cb - nca, static_cast<int>(blockIdx.z), s_hi, s_lo, s_row);
 }
 
 // Experts of several chunks: their partial gradients added in chunk order,
-// scaled and rounded once.  Experts without rows: zeros.  Block (e, part).
+// scaled and rounded once.  Experts without rows: zeros.  The blocks share the
+// quads (4 elements) of all these experts.
 __global__ __launch_bounds__(kBlock) void k_lora_join(WeightGradArgs a) {
+  __shared__ int s_e[1024], s_n[1024], s_first[1024];
+  __shared__ int s_count;
   if (!layout_current(a.status, a.generation)) return;
-  const int e = static_cast<int>(blockIdx.x);
-  const int n = (a.counts[e] + (1 << a.shift) - 1) >> a.shift;
-  if (n == 1) return;
-  int64_t first = 0;
-  if (n > 1) {
-    // tiles of experts with several tiles before this one
-    __shared__ int s_many[kWavesPerBlock];
-    int many = 0;
-    for (int i = threadIdx.x; i < e; i += kBlock) {
-      const int c = (a.counts[i] + (1 << a.shift) - 1) >> a.shift;
-      many += c > 1 ? c : 0;
-    }
+  if (threadIdx.x < kWave) {
+    const int lane = threadIdx.x;
+    int count = 0, first = 0;  // experts to join; chunks of those with several
+    for (int e0 = 0; e0 < a.E; e0 += kWave) {
+      const int e = e0 + lane;
+      const int n = e < a.E ? (a.counts[e] + (1 << a.shift) - 1) >> a.shift : 1;
+      const uint64_t todo = ballot(n != 1);
+      int incl = n > 1 ? n : 0;
 #pragma unroll
-    for (int off = kWave / 2; off > 0; off >>= 1) many += __shfl_xor(many, off, kWave);
-    if ((threadIdx.x & (kWave - 1)) == 0) s_many[threadIdx.x / kWave] = many;
-    __syncthreads();
-    for (int w = 0; w < kWavesPerBlock; ++w) first += s_many[w];
+      for (int off = 1; off < kWave; off <<= 1) {
+        const int v = __shfl_up(incl, off, kWave);
+        if (lane >= off) incl += v;
+      }
+      if (n != 1) {
+        const int at = count + __popcll(todo & lanemask_lt());
+        s_e[at] = e;
+        s_n[at] = n;
+        s_first[at] = first + incl - (n > 1 ? n : 0);
+      }
+      count += __popcll(todo);
+      first += readlane(incl, kWave - 1);
+    }
+    if (lane == 0) s_count = count;
   }
-  const float scale = a.scales ? a.scales[e] : 1.0f;
+  __syncthreads();
   const int64_t size_a = static_cast<int64_t>(a.R) * a.C[0];
   const int64_t size_b = static_cast<int64_t>(a.R) * a.C[1];
   const int64_t quads = a.slot_size / 4;  // R is a multiple of 8
-  for (int64_t i = static_cast<int64_t>(blockIdx.y) * kBlock + threadIdx.x; i < quads;
-       i += static_cast<int64_t>(gridDim.y) * kBlock) {
+  const int64_t parts = (quads + kBlock - 1) / kBlock;
+  for (int64_t b = blockIdx.x; b < parts * s_count; b += gridDim.x) {
+    const int k = static_cast<int>(b / parts);
+    const int64_t i = (b - k * parts) * kBlock + threadIdx.x;
+    if (i >= quads) continue;
+    const int64_t e = s_e[k];
+    const int n = s_n[k];
+    const float scale = a.scales ? a.scales[e] : 1.0f;
     f32x4_t sum = f32x4_t{};
-    for (int c = 0; c < n; ++c)
-      sum += *reinterpret_cast<const f32x4_t*>(a.slots + (first + c) * a.slot_size + 4 * i);
+    const float* p = a.slots + s_first[k] * a.slot_size + 4 * i;
+#pragma unroll 4
+    for (int c = 0; c < n; ++c) sum += *reinterpret_cast<const f32x4_t*>(p + c * a.slot_size);
     u32x2 o;
     o[0] = bf16x2_of(scale * sum[0], scale * sum[1]);
     o[1] = bf16x2_of(scale * sum[2], scale * sum[3]);
@@ -572,39 +832,47 @@ __global__ __launch_bounds__(kBlock) void k_lora_join(WeightGradArgs a) {
 }
 
 // ------------------------------------------------------------------ launches
+template <int RT, bool KMAJOR>
+hipError_t shrink_rt(const ShrinkArgs& a, const LoraGeom& g, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(g.max_tiles), static_cast<unsigned>(a.S));
+  constexpr int kMost = RT < 8 ? 4 : 2;  // registers
+  if (g.row_tiles == 1) k_lora_shrink<RT, 1, 8, KMAJOR><<<grid, 8 * kWave, 0, s>>>(a);
+  else if (g.row_tiles == 2) k_lora_shrink<RT, 2, 4, KMAJOR><<<grid, 4 * kWave, 0, s>>>(a);
+  else k_lora_shrink<RT, kMost, 4, KMAJOR><<<grid, 4 * kWave, 0, s>>>(a);
+  return hipGetLastError();
+}
+
 template <bool KMAJOR>
 hipError_t shrink(const ShrinkArgs& a, const LoraGeom& g, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(g.max_tiles), static_cast<unsigned>(a.S));
-  const int rt = (a.R + 15) / 16;
-  auto go = [&](auto k1, auto k2, auto k4) {
-    if (g.row_tiles == 1) k1<<<grid, kBlock, 0, s>>>(a);
-    else if (g.row_tiles == 2) k2<<<grid, kBlock, 0, s>>>(a);
-    else k4<<<grid, kBlock, 0, s>>>(a);
-    return hipGetLastError();
-  };
-  if (rt <= 1) return go(k_lora_shrink<1, 1, KMAJOR>, k_lora_shrink<1, 2, KMAJOR>, k_lora_shrink<1, 4, KMAJOR>);
-  if (rt <= 2) return go(k_lora_shrink<2, 1, KMAJOR>, k_lora_shrink<2, 2, KMAJOR>, k_lora_shrink<2, 4, KMAJOR>);
-  if (rt <= 4) return go(k_lora_shrink<4, 1, KMAJOR>, k_lora_shrink<4, 2, KMAJOR>, k_lora_shrink<4, 4, KMAJOR>);
-  return go(k_lora_shrink<8, 1, KMAJOR>, k_lora_shrink<8, 2, KMAJOR>, k_lora_shrink<8, 4, KMAJOR>);
+  if (a.R <= 16) return shrink_rt<1, KMAJOR>(a, g, s);
+  if (a.R <= 32) return shrink_rt<2, KMAJOR>(a, g, s);
+  if (a.R <= 64) return shrink_rt<4, KMAJOR>(a, g, s);
+  return shrink_rt<8, KMAJOR>(a, g, s);
 }
 
 template <bool JMAJOR>
 hipError_t expand(const ExpandArgs& a, const LoraGeom& g, hipStream_t s) {
   const unsigned ncb = static_cast<unsigned>((a.N + 4 * kCols - 1) / (4 * kCols));
-  const dim3 grid(static_cast<unsigned>(g.max_tiles), ncb + (a.map && a.base != a.out ? 1u : 0u));
-  auto go = [&](auto k1, auto k2, auto k4) {
-    if (g.row_tiles == 1) k1<<<grid, kBlock, 0, s>>>(a);
-    else if (g.row_tiles == 2) k2<<<grid, kBlock, 0, s>>>(a);
-    else k4<<<grid, kBlock, 0, s>>>(a);
-    return hipGetLastError();
+  const dim3 grid(ncb + (a.map && a.base != a.out ? 1u : 0u), static_cast<unsigned>(g.max_expand));
+  if (a.R <= 16) k_lora_expand<1, true, JMAJOR><<<grid, kBlock, 0, s>>>(a);
+  else if (a.R <= 32) k_lora_expand<1, false, JMAJOR><<<grid, kBlock, 0, s>>>(a);
+  else if (a.R <= 64) k_lora_expand<2, false, JMAJOR><<<grid, kBlock, 0, s>>>(a);
+  else k_lora_expand<4, false, JMAJOR><<<grid, kBlock, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int JT>
+hipError_t weight_grad(const WeightGradArgs& w, const LoraGeom& g, hipStream_t s) {
+  const unsigned chunks = static_cast<unsigned>(g.max_chunks);
+  const unsigned jg = static_cast<unsigned>((w.R + 16 * JT - 1) / (16 * JT));
+  auto blocks = [&](int nw) {
+    const int per = nw * kCols;
+    return static_cast<unsigned>((w.C[0] + per - 1) / per + (w.C[1] + per - 1) / per);
   };
-  if (a.R <= 16)
-    return go(k_lora_expand<1, 1, true, JMAJOR>, k_lora_expand<1, 2, true, JMAJOR>, k_lora_expand<1, 4, true, JMAJOR>);
-  if (a.R <= 32)
-    return go(k_lora_expand<1, 1, false, JMAJOR>, k_lora_expand<1, 2, false, JMAJOR>, k_lora_expand<1, 4, false, JMAJOR>);
-  if (a.R <= 64)
-    return go(k_lora_expand<2, 1, false, JMAJOR>, k_lora_expand<2, 2, false, JMAJOR>, k_lora_expand<2, 4, false, JMAJOR>);
-  return go(k_lora_expand<4, 1, false, JMAJOR>, k_lora_expand<4, 2, false, JMAJOR>, k_lora_expand<4, 4, false, JMAJOR>);
+  const size_t lds = sizeof(int) << g.chunk_shift;
+  if (g.chunk_waves == 1) k_lora_weight_grad<JT, 1><<<dim3(blocks(1), chunks, jg), kWave, lds, s>>>(w);
+  else k_lora_weight_grad<JT, 2><<<dim3(blocks(2), chunks, jg), 2 * kWave, lds, s>>>(w);
+  return hipGetLastError();
 }
 
 int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -614,6 +882,10 @@ ShrinkArgs shrink_args(const LoraArgs& a, const LoraGeom& g) {
   s.R = a.R;
   s.E = a.E;
   s.stride = g.rows * a.R;
+  s.tiles = a.tiles;
+  s.expand_tiles = a.expand_tiles;
+  s.num_expand = static_cast<int>(g.max_expand);
+  s.expand_shift = g.expand_shift;
   s.counts = a.counts;
   s.offsets = a.offsets;
   s.status = a.status;
@@ -633,9 +905,7 @@ ExpandArgs expand_args(const LoraArgs& a, const LoraGeom& g) {
   x.slot = a.slot;
   x.T = a.T;
   x.R = a.R;
-  x.E = a.E;
-  x.counts = a.counts;
-  x.offsets = a.offsets;
+  x.tiles = a.expand_tiles;
   x.status = a.status;
   x.generation = a.generation;
   return x;
@@ -648,25 +918,41 @@ LoraGeom lora_geom(int64_t rows, int E, int H, int N, int R, bool backward) {
   g.rows = rows;
   const int64_t used = rows < E ? rows : E;  // experts with rows, at most
   const int64_t avg = rows / E;
-  g.row_tiles = avg >= 64 ? 4 : avg >= 32 ? 2 : 1;
-  g.max_tiles = rows / (16 * g.row_tiles) + used;
-  // enough blocks for every CU twice, of at least 256 of the contraction
+  auto up8 = [](int64_t n) { return (n + kXcds - 1) / kXcds * kXcds; };
+  // Tiles of 64 rows read an expert's matrix least often; smaller ones where
+  // its rows, or all rows, are few.
+  const int64_t wide = R <= 64 ? 4 : 2;  // registers
+  int64_t tiles = avg >= 64 ? 4 : avg >= 32 ? 2 : 1;
+  if (rows < 2048) tiles = 1;
+  else if (rows < 4096 && tiles > 2) tiles = 2;
+  g.row_tiles = static_cast<int>(tiles < wide ? tiles : wide);
+  g.max_tiles = up8(rows / (16 * g.row_tiles) + used);
+  g.tile_bytes = static_cast<size_t>(g.max_tiles) * 16;
+  // the contraction is split over blocks too until there are two per CU
   auto splits = [&](int C) {
-    int64_t s = 512 / (g.max_tiles > 0 ? g.max_tiles : 1);
-    const int64_t most = C / 256 > 0 ? C / 256 : 1;
-    if (s > most) s = most;
-    return static_cast<int>(s < 1 ? 1 : s > 16 ? 16 : s);
+    int n = 1;
+    while (n < kMaxSplits && g.max_tiles * n < 512 && C >= 512 * n) n *= 2;
+    return n;
   };
+  // The result's tiles: the longest that leave about two blocks per CU
+  const int64_t col_blocks = ((backward ? H : N) + 4 * kCols - 1) / (4 * kCols);
+  auto expand_tiles = [&](int shift) { return up8((rows >> shift) + used); };
+  g.expand_shift = R <= 64 ? 7 : 6;
+  while (g.expand_shift > 4 && expand_tiles(g.expand_shift) * col_blocks < 500) --g.expand_shift;
+  g.max_expand = expand_tiles(g.expand_shift);
+  g.expand_bytes = static_cast<size_t>(g.max_expand) * 16;
   g.split_x = splits(H);
   g.u_bytes = static_cast<size_t>(up16(g.split_x * rows * R * 4));
   if (backward) {
     g.split_g = splits(N);
     g.v_bytes = static_cast<size_t>(up16(g.split_g * rows * R * 4));
-    g.chunk_shift = 6;
-    while ((static_cast<int64_t>(32) << g.chunk_shift) < rows) ++g.chunk_shift;
-    g.max_chunks = (rows >> g.chunk_shift) + used;
+    g.chunk_shift = 7;
+    while (g.chunk_shift < 12 && (static_cast<int64_t>(32) << g.chunk_shift) < rows) ++g.chunk_shift;
+    g.max_chunks = up8((rows >> g.chunk_shift) + used);
+    g.chunk_bytes = static_cast<size_t>(g.max_chunks) * 16;
+    g.chunk_waves = g.max_chunks * ((H + N) / kCols) < 2048 ? 1 : 2;
     // an expert of several chunks has more than one chunk of rows, so its
-    // chunks are fewer than twice its rows over the chunk size
+    // chunks are at most twice its rows over the chunk size
     g.slots = 2 * (rows >> g.chunk_shift);
     g.slot_bytes = static_cast<size_t>(g.slots) * R * (static_cast<size_t>(H) + N) * 4;
   }
@@ -704,8 +990,12 @@ hipError_t row_gradients(const LoraArgs& a, const LoraGeom& g, hipStream_t s) {
   sh.C = a.H;
   sh.part = a.u;
   sh.S = g.split_x;
+  sh.chunks = a.chunks;
+  sh.num_chunks = static_cast<int>(g.max_chunks);
+  sh.chunk_shift = g.chunk_shift;
   hipError_t err = shrink<false>(sh, g, s);
   if (err != hipSuccess) return err;
+  sh.known = true;
   sh.in = a.go;
   sh.ld = a.ldgo;
   sh.map = a.omap;
@@ -752,23 +1042,19 @@ hipError_t launch_lora_backward(const LoraArgs& a, const LoraGeom& g, hipStream_
   w.R = a.R;
   w.E = a.E;
   w.shift = g.chunk_shift;
+  w.chunks = a.chunks;
   w.counts = a.counts;
-  w.offsets = a.offsets;
   w.status = a.status;
   w.generation = a.generation;
-  const int per = 4 * kCols;
-  const unsigned cb = static_cast<unsigned>((a.H + per - 1) / per + (a.N + per - 1) / per);
-  const unsigned chunks = static_cast<unsigned>(g.max_chunks);
-  if (chunks > 0) {
-    if (a.R <= 16) k_lora_weight_grad<1><<<dim3(chunks, cb, 1), kBlock, 0, s>>>(w);
-    else if (a.R <= 32) k_lora_weight_grad<2><<<dim3(chunks, cb, 1), kBlock, 0, s>>>(w);
-    else k_lora_weight_grad<4><<<dim3(chunks, cb, a.R <= 64 ? 1 : 2), kBlock, 0, s>>>(w);
-    const hipError_t err = hipGetLastError();
+  if (g.rows > 0) {
+    hipError_t err;
+    if (a.R <= 16) err = weight_grad<1>(w, g, s);
+    else if (a.R <= 32) err = weight_grad<2>(w, g, s);
+    else err = weight_grad<4>(w, g, s);
     if (err != hipSuccess) return err;
   }
-  int64_t parts = w.slot_size / 4 / kBlock / 4;  // 4 quads per thread
-  parts = parts < 1 ? 1 : parts > 256 ? 256 : parts;
-  k_lora_join<<<dim3(static_cast<unsigned>(a.E), static_cast<unsigned>(parts)), kBlock, 0, s>>>(w);
+  const int64_t parts = (w.slot_size / 4 + kBlock - 1) / kBlock * a.E;
+  k_lora_join<<<static_cast<unsigned>(parts < 1024 ? parts : 1024), kBlock, 0, s>>>(w);
   return hipGetLastError();
 }
 
