@@ -79,10 +79,9 @@ struct LoraGeom {
   int chunk_shift;    // log2 of the rows of a weight-gradient chunk
   int64_t max_chunks;  // weight-gradient chunks at most
   int64_t slots;       // partial gradients of experts with several chunks, at most
-  int chunk_waves;     // waves per block of the weight gradients
   // workspace parts, multiples of 16
-  size_t tile_bytes, expand_bytes, chunk_bytes, u_bytes, v_bytes, slot_bytes;
-  size_t bytes() const { return tile_bytes + expand_bytes + chunk_bytes + u_bytes + v_bytes + slot_bytes; }
+  size_t expand_bytes, chunk_bytes, u_bytes, v_bytes, slot_bytes;
+  size_t bytes() const { return expand_bytes + chunk_bytes + u_bytes + v_bytes + slot_bytes; }
 };
 LoraGeom lora_geom(int64_t rows, int E, int H, int N, int R, bool backward);
 
@@ -108,15 +107,16 @@ struct LoraArgs {
   int64_t ldgo;
   uint16_t* ga;  // [E, R, H]
   uint16_t* gb;  // [E, N, R]
-  int32_t* tiles;         // workspace: 4 words per row tile,
-  int32_t* expand_tiles;  // tile of the result
-  int32_t* chunks;        // and weight-gradient chunk
+  int32_t* expand_tiles;  // workspace: 4 words per tile of the result
+  int32_t* chunks;        // and per weight-gradient chunk
   float* u;      // split_x partial sums of [rows, R]
   float* v;      // split_g partial sums of [rows, R]
   float* slots;  // partial gradients
   int32_t* status;
   uint32_t generation;
 };
+// blocks of the weight gradients
+int64_t lora_weight_blocks(const LoraGeom& g, int H, int N, int R);
 hipError_t launch_lora(const LoraArgs& a, const LoraGeom& g, hipStream_t s);
 hipError_t launch_lora_backward(const LoraArgs& a, const LoraGeom& g, hipStream_t s);
 

@@ -77,6 +77,10 @@ int64_t max_rows(const ep_problem_t* p) {
   return p->num_tokens * p->topk + pad;
 }
 
+ep::LoraGeom geom_of(const ep_problem_t* p, const ep_lora_weights_t* w, bool backward) {
+  return ep::lora_geom(max_rows(p), p->num_experts, p->hidden, w->n_out, w->rank, backward);
+}
+
 // Problem, adapters and sizes of both adapter calls.
 int check_lora(const ep_problem_t* p, const ep_lora_weights_t* w) {
   const int rc = check_problem(p);
@@ -85,15 +89,14 @@ int check_lora(const ep_problem_t* p, const ep_lora_weights_t* w) {
   if ((w->flags & EP_LORA_SCATTER_ROWS) && p->topk != 1) return EP_EINVAL;
   if (p->hidden % 8 != 0 || w->n_out % 8 != 0 || w->rank % 8 != 0 || w->rank > EP_MAX_LORA_RANK)
     return EP_ENOTSUP;
-  // grid limits: 2^24 tiles of at least 16 rows, 65,534 blocks of 512 columns
-  const int64_t rows = max_rows(p);
-  if (rows / 16 + p->num_experts >= (1 << 24)) return EP_ENOTSUP;
-  if (static_cast<int64_t>(p->hidden) + w->n_out > 65500LL * 512) return EP_ENOTSUP;
+  // grid limits: fewer than 2^32 threads, and 2^31 row indices (check_problem)
+  if (static_cast<int64_t>(p->hidden) + w->n_out > (1 << 24)) return EP_ENOTSUP;
+  const ep::LoraGeom g = geom_of(p, w, true);
+  const int64_t cols = (p->hidden > w->n_out ? p->hidden : w->n_out) / 512 + 2;
+  if (g.max_tiles >= (1 << 23) ||
+      g.max_expand * cols + ep::lora_weight_blocks(g, p->hidden, w->n_out, w->rank) >= (1 << 24))
+    return EP_ENOTSUP;
   return EP_OK;
-}
-
-ep::LoraGeom geom_of(const ep_problem_t* p, const ep_lora_weights_t* w, bool backward) {
-  return ep::lora_geom(max_rows(p), p->num_experts, p->hidden, w->n_out, w->rank, backward);
 }
 
 // Layout, maps and adapters common to both adapter calls.
@@ -128,7 +131,6 @@ void set_workspace(ep::LoraArgs* a, const ep::LoraGeom& g, void* workspace) {
     ws += bytes;
     return at;
   };
-  a->tiles = reinterpret_cast<int32_t*>(part(g.tile_bytes));
   a->expand_tiles = reinterpret_cast<int32_t*>(part(g.expand_bytes));
   a->chunks = reinterpret_cast<int32_t*>(part(g.chunk_bytes));
   a->u = reinterpret_cast<float*>(part(g.u_bytes));

@@ -172,10 +172,8 @@ struct ShrinkArgs {
   float* part;     // [S, rows, R]
   int64_t stride;  // rows * R
   int S;
-  int32_t* tiles;  // written by the blocks of split 0, or (known) read
-  bool known;
-  // the same for the kernels to come, written by two waves of these blocks
-  int32_t* expand_tiles;
+  // tiles of the kernels to come, written by two waves of split 0's blocks
+  int32_t* expand_tiles;  // num_expand == 0: none
   int num_expand, expand_shift;
   int32_t* chunks;  // num_chunks == 0: none
   int num_chunks, chunk_shift;
@@ -185,7 +183,6 @@ struct ShrinkArgs {
   uint32_t generation;
 };
 
-constexpr int kStageBlocks = 256;  // 8 x 8 blocks of a k-major matrix staged at a time
 
 // Block: one row tile (16 MT rows) and one split of the contraction, whose
 // 64-wide pieces the NW waves take in turn, the next piece's loads in flight
@@ -193,22 +190,29 @@ constexpr int kStageBlocks = 256;  // 8 x 8 blocks of a k-major matrix staged at
 // waves a block: several blocks share a CU, and one's start and end hide
 // behind another's loads.
 template <int RT, int MT, int NW, bool KMAJOR>
-__global__ __launch_bounds__(NW* kWave) void k_lora_shrink(ShrinkArgs a) {
+struct ShrinkLds {
+  // one wave's sums
+  static constexpr int kPitch = RT * 16 + 4;
+  static constexpr int kRed = MT * 16 * kPitch;
+  // k-major: 32 KiB of the matrix as 8 x 8 blocks, transposed: RT * 16 rows of
+  // kStage (and 8, so that rows start on different banks)
+  static constexpr int kBlocks = 256;
+  static constexpr int kStage = kBlocks * 64 / (RT * 16);
+  static constexpr int kWBytes = KMAJOR ? RT * 16 * (kStage + 8) * 2 : 0;
+  static constexpr int kXBytes = NW * (KMAJOR ? MT : MT + RT) * 2048;
+  static constexpr int kBytes = NW * kRed * 4 > kWBytes + kXBytes ? NW * kRed * 4 : kWBytes + kXBytes;
+};
+
+template <int RT, int MT, int NW, bool KMAJOR>
+__device__ __forceinline__ void shrink(const ShrinkArgs& a, char* s_mem) {
+  using Lds = ShrinkLds<RT, MT, NW, KMAJOR>;
   constexpr int kShift = MT == 1 ? 4 : MT == 2 ? 5 : 6;
-  constexpr int kPitch = RT * 16 + 4;
-  // k-major: 32 KiB of the matrix, transposed: RT * 16 rows of kStage (and 8,
-  // so that rows start on different banks)
-  constexpr int kStage = kStageBlocks * 64 / (RT * 16);
-  constexpr int kRed = MT * 16 * kPitch;  // one wave's sums
-  constexpr int kRedBytes = NW * kRed * 4;
-  constexpr int kXBytes = NW * (KMAJOR ? MT : MT + RT) * 2048;
-  constexpr int kWBytes = KMAJOR ? RT * 16 * (kStage + 8) * 2 : 0;
-  __shared__ __align__(16) char s_mem[kRedBytes > kWBytes + kXBytes ? kRedBytes : kWBytes + kXBytes];
+  constexpr int kPitch = Lds::kPitch, kRed = Lds::kRed, kStage = Lds::kStage, kWBytes = Lds::kWBytes;
   if (!layout_current(a.status, a.generation)) return;
+  if (static_cast<int>(blockIdx.y) >= a.S) return;
   const int block = static_cast<int>(blockIdx.x);
-  const Tile t = a.known ? stored_tile(a.tiles, block) : find_tile<true>(a.counts, a.offsets, a.E, kShift, block);
-  if (!a.known && blockIdx.y == 0) {
-    if (threadIdx.x == 0) store_tile(a.tiles, block, t);
+  const Tile t = find_tile<true>(a.counts, a.offsets, a.E, kShift, block);
+  if (blockIdx.y == 0) {
     const int w = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
     auto table = [&](int32_t* out, int n, int shift) {
       for (int b = block; b < n; b += static_cast<int>(gridDim.x)) {
@@ -268,13 +272,11 @@ __global__ __launch_bounds__(NW* kWave) void k_lora_shrink(ShrinkArgs a) {
     for (int n = 0; n < 2 * MT; ++n) put(s_x, n, past(p) ? u32x4{0u, 0u, 0u, 0u} : x[n]);
   };
   if constexpr (!KMAJOR) {
-    const uint16_t* wr[2 * RT];
-#pragma unroll
-    for (int n = 0; n < 2 * RT; ++n)  // rows past R repeat the last, and are dropped
-      wr[n] = w + static_cast<int64_t>(min(n * 8 + l8, a.R - 1)) * a.C + unit * 8;
+    const uint16_t* wr = w + static_cast<int64_t>(l8) * a.C + unit * 8;
     auto load_w = [&](int p, u32x4 (&v)[2 * RT]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int n = 0; n < 2 * RT; ++n) v[n] = load16(wr[n] + place(p));
+      for (int n = 0; n < 2 * RT; ++n)  // rows past R (a multiple of 8) repeat the last 8, and are dropped
+        v[n] = load16(wr + static_cast<int64_t>(min(n * 8, a.R - 8)) * a.C + place(p));
     };
     u32x4 x[2 * MT], v[2 * RT];
     int p = p0 + wave;
@@ -317,7 +319,7 @@ __global__ __launch_bounds__(NW* kWave) void k_lora_shrink(ShrinkArgs a) {
       if (k < q1) load_x(k / 64, x);
       // 8 x 8 blocks (8 k, 8 of R) transposed in registers, k contiguous in LDS
       if (k0 > p0 * 64) __syncthreads();
-      for (int b = threadIdx.x; b < kStageBlocks; b += NW * kWave) {
+      for (int b = threadIdx.x; b < Lds::kBlocks; b += NW * kWave) {
         const int jb = b % (RT * 2), kb = b / (RT * 2);
         const int kk = k0 + kb * 8;
         u32x4 v[8], c[8];
@@ -372,6 +374,23 @@ __global__ __launch_bounds__(NW* kWave) void k_lora_shrink(ShrinkArgs a) {
   }
 }
 
+template <int RT, int MT, int NW>
+__global__ __launch_bounds__(NW* kWave) void k_lora_shrink(ShrinkArgs a) {
+  __shared__ __align__(16) char s_mem[ShrinkLds<RT, MT, NW, false>::kBytes];
+  shrink<RT, MT, NW, false>(a, s_mem);
+}
+
+// u and v of the backward pass in one launch: 509 rows x 4096, rank 8: 7.1 us
+// against 6.0 and 5.5 us in two; 16,384 rows x 4096 -> 2048, rank 32: 55 us
+// against 40 and 23 us.
+template <int RT, int MT, int NW>
+__global__ __launch_bounds__(NW* kWave) void k_lora_shrink_both(ShrinkArgs u, ShrinkArgs v) {
+  constexpr int kU = ShrinkLds<RT, MT, NW, false>::kBytes, kV = ShrinkLds<RT, MT, NW, true>::kBytes;
+  __shared__ __align__(16) char s_mem[kU > kV ? kU : kV];
+  if (blockIdx.z == 0) shrink<RT, MT, NW, false>(u, s_mem);
+  else shrink<RT, MT, NW, true>(v, s_mem);
+}
+
 // ------------------------------------------------------------------- expand
 struct ExpandArgs {
   const float* part;  // [S, rows, R]
@@ -388,20 +407,25 @@ struct ExpandArgs {
   int64_t T;
   int N, R;
   const int32_t* tiles;
+  int64_t num_tiles;
   int32_t* status;
   uint32_t generation;
 };
 
 // Rows of out that belong to no selection (token rows only): base's row, or
-// zeros.  32 tokens per block.
-__device__ __forceinline__ void copy_unselected(const ExpandArgs& a, int64_t t0, int wave, int lane) {
-  for (int i = 0; i < 8; ++i) {
-    const int64_t t = t0 + wave * 8 + i;
-    if (t >= a.T || a.slot[t] >= 0) continue;
-    for (int n = lane * 8; n < a.N; n += kWave * 8) {
-      u32x4 v = {0u, 0u, 0u, 0u};
-      if (a.base) v = load16(a.base + t * a.ldbase + n);
-      *reinterpret_cast<u32x4*>(a.out + t * a.ldout + n) = v;
+// zeros.  A block takes 32 tokens from t0, then from t0 + step, ...
+__device__ __forceinline__ void copy_unselected(const ExpandArgs& a, int64_t t0, int64_t step) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+  for (; t0 < a.T; t0 += step) {
+    for (int i = 0; i < 8; ++i) {
+      const int64_t t = t0 + wave * 8 + i;
+      if (t >= a.T || a.slot[t] >= 0) continue;
+      for (int n = lane * 8; n < a.N; n += kWave * 8) {
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (a.base) v = load16(a.base + t * a.ldbase + n);
+        *reinterpret_cast<u32x4*>(a.out + t * a.ldout + n) = v;
+      }
     }
   }
 }
@@ -462,25 +486,27 @@ __host__ __device__ constexpr int expand_rows(int KS) { return KS <= 2 ? 128 : 6
 // order, and with a load or store that may be skipped the compiler waits for
 // all of them instead of counting.  PACK: R <= 16, the high parts in the first
 // half of one contraction step and the low parts in the second.
+template <int KS, bool PACK>
+struct ExpandLds {
+  static constexpr int kPitch = KS * 32 + 8;
+  static constexpr int kStaged = expand_rows(KS);
+  static constexpr int kU = kStaged * kPitch;  // elements of one part
+  static constexpr int kBytes = (PACK ? 1 : 2) * kU * 2 + kStaged * 4;
+};
+
 template <int KS, bool PACK, bool JMAJOR>
-__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(KS == 1 ? 3 : 2))) void k_lora_expand(
-    ExpandArgs a) {
-  if (!layout_current(a.status, a.generation)) return;
+__device__ __forceinline__ void expand(const ExpandArgs& a, int64_t index, int col_block, char* s_mem) {
+  using Lds = ExpandLds<KS, PACK>;
+  constexpr int kPitch = Lds::kPitch, kStaged = Lds::kStaged;
+  uint16_t* const s_hi = reinterpret_cast<uint16_t*>(s_mem);
+  uint16_t* const s_lo = s_hi + (PACK ? 16 : Lds::kU);  // PACK: behind the high parts of each row
+  int* const s_row = reinterpret_cast<int*>(s_mem + (PACK ? 1 : 2) * Lds::kU * 2);
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
-  constexpr int kPitch = KS * 32 + 8;
-  constexpr int kStaged = expand_rows(KS);
-  __shared__ __align__(16) uint16_t s_u[PACK ? 1 : 2][kStaged * kPitch];
-  __shared__ int s_row[kStaged];
-  const int ncb = (a.N + 4 * kCols - 1) / (4 * kCols);
-  if (static_cast<int>(blockIdx.x) == ncb) {  // the column of rows of no selection
-    for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * 32; t0 < a.T; t0 += static_cast<int64_t>(gridDim.y) * 32)
-      copy_unselected(a, t0, wave, lane);
-    return;
-  }
-  const Tile t = stored_tile(a.tiles, static_cast<int>(blockIdx.y));
+  if (index >= a.num_tiles) return;
+  const Tile t = stored_tile(a.tiles, static_cast<int>(index));
   if (t.e < 0) return;
-  const int n0 = (static_cast<int>(blockIdx.x) * 4 + wave) * kCols;
+  const int n0 = (col_block * 4 + wave) * kCols;
   const int l16 = lane & 15, q = lane >> 4;
   const float scale = a.scales ? a.scales[t.e] : 1.0f;
   const uint16_t* w = a.w + static_cast<int64_t>(t.e) * a.R * a.N;
@@ -526,8 +552,8 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(KS == 1 
         const int r = i / kQuads, j = i % kQuads * 4;
         u32x2 hi, lo;
         split4(f, hi, lo);
-        *reinterpret_cast<u32x2*>(&s_u[0][r * kPitch + j]) = hi;
-        *reinterpret_cast<u32x2*>(PACK ? &s_u[0][r * kPitch + 16 + j] : &s_u[PACK ? 0 : 1][r * kPitch + j]) = lo;
+        *reinterpret_cast<u32x2*>(s_hi + r * kPitch + j) = hi;
+        *reinterpret_cast<u32x2*>(s_lo + r * kPitch + j) = lo;
       });
   __syncthreads();
   if (n0 >= a.N) return;
@@ -550,7 +576,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(KS == 1 
       const int at = (m * 16 + l16) * kPitch + ks * 32 + q * 8;
 #pragma unroll
       for (int d = 0; d < (PACK ? 1 : 2); ++d) {
-        const u32x4 u = *reinterpret_cast<const u32x4*>(&s_u[d][at]);
+        const u32x4 u = *reinterpret_cast<const u32x4*>((d == 0 ? s_hi : s_lo) + at);
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[c] = mfma(u, wv[ks][c], acc[c]);
       }
@@ -608,6 +634,20 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(KS == 1 
   }
 }
 
+template <int KS, bool PACK>
+__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(KS == 1 ? 3 : 2))) void k_lora_expand(
+    ExpandArgs a) {
+  __shared__ __align__(16) char s_mem[ExpandLds<KS, PACK>::kBytes];
+  if (!layout_current(a.status, a.generation)) return;
+  const int64_t index = static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y;
+  const int ncb = (a.N + 4 * kCols - 1) / (4 * kCols);
+  if (static_cast<int>(blockIdx.x) == ncb) {  // the column of rows of no selection
+    copy_unselected(a, index * 32, static_cast<int64_t>(gridDim.y) * gridDim.z * 32);
+    return;
+  }
+  expand<KS, PACK, false>(a, index, static_cast<int>(blockIdx.x), s_mem);
+}
+
 // --------------------------------------------------------- weight gradients
 struct WeightGradArgs {
   // [0]: dA from x and v, [1]: dB from g and u
@@ -633,7 +673,7 @@ struct WeightGradArgs {
 __host__ __device__ constexpr int staged_rows(int JT) { return 256 / JT; }
 
 // Block: one chunk of an expert's rows, 128 NW columns of x (or g), 16 JT of the
-// R.  A wave takes 32 rows by 128 columns per step, two steps in flight, loaded
+// R.  A wave takes 32 rows by 128 columns per step, one or two steps in flight, loaded
 // without a condition (see k_lora_expand).  A lane ends with R's 4 q + i (i < 4)
 // of each 16 and 8 neighbouring columns.
 template <int JT, int NW, int B>
@@ -663,9 +703,10 @@ __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile&
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = load16(in + s_row[min(r + q * 8 + i, t.nrows - 1)] * a.ld[B]);
   };
-  u32x4 v[2][8];
-  load_step(0, v[0]);
-  load_step(32, v[1]);
+  constexpr int kAhead = JT <= 2 ? 2 : 1;  // steps in flight, as registers allow
+  u32x4 v[kAhead][8];
+#pragma unroll
+  for (int d = 0; d < kAhead; ++d) load_step(32 * d, v[d]);
   for (int r0 = 0; r0 < t.nrows; r0 += kStaged) {
     if (r0 > 0) __syncthreads();  // the rows staged before are used up
     const int staged = min(kStaged, (t.nrows - r0 + 63) / 64 * 64);
@@ -687,9 +728,9 @@ __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile&
           }
         });
     __syncthreads();
-    for (int r = 0; r < staged; r += 64) {
+    for (int r = 0; r < staged; r += 32 * kAhead) {
 #pragma unroll
-      for (int d = 0; d < 2; ++d) {
+      for (int d = 0; d < kAhead; ++d) {
         const int at_row = r0 + r + d * 32;
         if (at_row + 32 > t.nrows) {  // rows past the chunk are zeros in both operands
 #pragma unroll
@@ -698,7 +739,7 @@ __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile&
         }
         u32x4 cv[8];
         columns(v[d], cv);
-        load_step(at_row + 64, v[d]);
+        load_step(at_row + 32 * kAhead, v[d]);
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
           const int at = (j * 16 + l16) * kPitch + r + d * 32 + q * 8;
@@ -760,24 +801,44 @@ __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile&
   }
 }
 
-template <int JT, int NW>
-__global__ __launch_bounds__(NW* kWave) void k_lora_weight_grad(WeightGradArgs a) {
+// dA, dB and dx in one launch: all need u and v and no more.  The first
+// blocks take the weight gradients, the longer work, the others tiles of dx.
+template <int KS, bool PACK, int JT>
+__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(2))) void k_lora_gradients(
+    WeightGradArgs w, ExpandArgs x, unsigned weight_blocks, int copy) {
   constexpr int kElems = JT * 16 * (staged_rows(JT) + 8);
-  __shared__ __align__(16) uint16_t s_hi[kElems];
-  __shared__ __align__(16) uint16_t s_lo[kElems];
+  constexpr int kW = 4 * kElems, kX = ExpandLds<KS, PACK>::kBytes;
+  __shared__ __align__(16) char s_mem[kW > kX ? kW : kX];
   extern __shared__ int s_row[];  // a chunk's rows
-  if (!layout_current(a.status, a.generation)) return;
-  const Tile t = stored_tile(a.chunks, static_cast<int>(blockIdx.y));
-  if (t.e < 0) return;
-  const int nca = (a.C[0] + NW * kCols - 1) / (NW * kCols);
-  const int cb = static_cast<int>(blockIdx.x);
-  if (cb < nca) weight_grad<JT, NW, 0>(a, t, cb, static_cast<int>(blockIdx.z), s_hi, s_lo, s_row);
-  else weight_grad<JT, NW, 1>(a, t, cb - nca, static_cast<int>(blockIdx.z), s_hi, s_lo, s_row);
+  if (!layout_current(w.status, w.generation)) return;
+  if (blockIdx.x < weight_blocks) {
+    constexpr int kPer = kWavesPerBlock * kCols;
+    const int nca = (w.C[0] + kPer - 1) / kPer, ncb = (w.C[1] + kPer - 1) / kPer;
+    const int jgs = (w.R + 16 * JT - 1) / (16 * JT);
+    // columns fastest: blocks of a chunk read its rows together
+    const int cols = nca + ncb;
+    int at = static_cast<int>(blockIdx.x);
+    const int cb = at % cols;
+    at /= cols;
+    const int jg = at % jgs;
+    const Tile t = stored_tile(w.chunks, at / jgs);
+    if (t.e < 0) return;
+    uint16_t* const s_hi = reinterpret_cast<uint16_t*>(s_mem);
+    if (cb < nca) weight_grad<JT, kWavesPerBlock, 0>(w, t, cb, jg, s_hi, s_hi + kElems, s_row);
+    else weight_grad<JT, kWavesPerBlock, 1>(w, t, cb - nca, jg, s_hi, s_hi + kElems, s_row);
+  } else {
+    const int ncb = (x.N + 4 * kCols - 1) / (4 * kCols);
+    const int cols = ncb + copy;
+    const int at = static_cast<int>(blockIdx.x - weight_blocks);
+    const int cb = at % cols;
+    if (cb == ncb) copy_unselected(x, static_cast<int64_t>(at / cols) * 32, x.num_tiles * 32);
+    else expand<KS, PACK, true>(x, at / cols, cb, s_mem);
+  }
 }
 
 // Experts of several chunks: their partial gradients added in chunk order,
-// scaled and rounded once.  Experts without rows: zeros.  The blocks share the
-// quads (4 elements) of all these experts.
+// scaled and rounded once.  Experts without rows: zeros.  Blocks (part of an
+// expert's quads, of 4 elements; every 8th of these experts).
 __global__ __launch_bounds__(kBlock) void k_lora_join(WeightGradArgs a) {
   __shared__ int s_e[1024], s_n[1024], s_first[1024];
   __shared__ int s_count;
@@ -810,68 +871,76 @@ __global__ __launch_bounds__(kBlock) void k_lora_join(WeightGradArgs a) {
   const int64_t size_a = static_cast<int64_t>(a.R) * a.C[0];
   const int64_t size_b = static_cast<int64_t>(a.R) * a.C[1];
   const int64_t quads = a.slot_size / 4;  // R is a multiple of 8
-  const int64_t parts = (quads + kBlock - 1) / kBlock;
-  for (int64_t b = blockIdx.x; b < parts * s_count; b += gridDim.x) {
-    const int k = static_cast<int>(b / parts);
-    const int64_t i = (b - k * parts) * kBlock + threadIdx.x;
-    if (i >= quads) continue;
+  for (int k = static_cast<int>(blockIdx.y); k < s_count; k += static_cast<int>(gridDim.y)) {
     const int64_t e = s_e[k];
     const int n = s_n[k];
     const float scale = a.scales ? a.scales[e] : 1.0f;
-    f32x4_t sum = f32x4_t{};
-    const float* p = a.slots + s_first[k] * a.slot_size + 4 * i;
-#pragma unroll 4
-    for (int c = 0; c < n; ++c) sum += *reinterpret_cast<const f32x4_t*>(p + c * a.slot_size);
-    u32x2 o;
-    o[0] = bf16x2_of(scale * sum[0], scale * sum[1]);
-    o[1] = bf16x2_of(scale * sum[2], scale * sum[3]);
-    if (n == 0) o = u32x2{0u, 0u};
-    uint16_t* out = 4 * i < size_a ? a.out[0] + e * size_a + 4 * i : a.out[1] + e * size_b + (4 * i - size_a);
-    *reinterpret_cast<u32x2*>(out) = o;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; i < quads;
+         i += static_cast<int64_t>(gridDim.x) * kBlock) {
+      f32x4_t sum = f32x4_t{};
+      const float* p = a.slots + s_first[k] * a.slot_size + 4 * i;
+#pragma unroll 8
+      for (int c = 0; c < n; ++c) sum += *reinterpret_cast<const f32x4_t*>(p + c * a.slot_size);
+      u32x2 o;
+      o[0] = bf16x2_of(scale * sum[0], scale * sum[1]);
+      o[1] = bf16x2_of(scale * sum[2], scale * sum[3]);
+      if (n == 0) o = u32x2{0u, 0u};
+      uint16_t* out = 4 * i < size_a ? a.out[0] + e * size_a + 4 * i : a.out[1] + e * size_b + (4 * i - size_a);
+      *reinterpret_cast<u32x2*>(out) = o;
+    }
   }
 }
 
 // ------------------------------------------------------------------ launches
-template <int RT, bool KMAJOR>
-hipError_t shrink_rt(const ShrinkArgs& a, const LoraGeom& g, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(g.max_tiles), static_cast<unsigned>(a.S));
+template <int RT, int MT, int NW>
+void shrink_mt(const ShrinkArgs& u, const ShrinkArgs* v, const LoraGeom& g, hipStream_t s) {
+  const int splits = v && v->S > u.S ? v->S : u.S;
+  const dim3 grid(static_cast<unsigned>(g.max_tiles), static_cast<unsigned>(splits), v ? 2 : 1);
+  if (v) k_lora_shrink_both<RT, MT, NW><<<grid, NW * kWave, 0, s>>>(u, *v);
+  else k_lora_shrink<RT, MT, NW><<<grid, NW * kWave, 0, s>>>(u);
+}
+
+template <int RT>
+void shrink_rt(const ShrinkArgs& u, const ShrinkArgs* v, const LoraGeom& g, hipStream_t s) {
   constexpr int kMost = RT < 8 ? 4 : 2;  // registers
-  if (g.row_tiles == 1) k_lora_shrink<RT, 1, 8, KMAJOR><<<grid, 8 * kWave, 0, s>>>(a);
-  else if (g.row_tiles == 2) k_lora_shrink<RT, 2, 4, KMAJOR><<<grid, 4 * kWave, 0, s>>>(a);
-  else k_lora_shrink<RT, kMost, 4, KMAJOR><<<grid, 4 * kWave, 0, s>>>(a);
+  if (g.row_tiles == 1) shrink_mt<RT, 1, 8>(u, v, g, s);
+  else if (g.row_tiles == 2) shrink_mt<RT, 2, 4>(u, v, g, s);
+  else shrink_mt<RT, kMost, 4>(u, v, g, s);
+}
+
+// u, and v where it is wanted
+hipError_t launch_shrink(const ShrinkArgs& u, const ShrinkArgs* v, const LoraGeom& g, hipStream_t s) {
+  if (u.R <= 16) shrink_rt<1>(u, v, g, s);
+  else if (u.R <= 32) shrink_rt<2>(u, v, g, s);
+  else if (u.R <= 64) shrink_rt<4>(u, v, g, s);
+  else shrink_rt<8>(u, v, g, s);
   return hipGetLastError();
 }
 
-template <bool KMAJOR>
-hipError_t shrink(const ShrinkArgs& a, const LoraGeom& g, hipStream_t s) {
-  if (a.R <= 16) return shrink_rt<1, KMAJOR>(a, g, s);
-  if (a.R <= 32) return shrink_rt<2, KMAJOR>(a, g, s);
-  if (a.R <= 64) return shrink_rt<4, KMAJOR>(a, g, s);
-  return shrink_rt<8, KMAJOR>(a, g, s);
-}
+// Is there a row of no selection to write?
+bool copies(const ExpandArgs& a) { return a.map && a.base != a.out; }
 
-template <bool JMAJOR>
-hipError_t expand(const ExpandArgs& a, const LoraGeom& g, hipStream_t s) {
+hipError_t launch_expand(const ExpandArgs& a, hipStream_t s) {
   const unsigned ncb = static_cast<unsigned>((a.N + 4 * kCols - 1) / (4 * kCols));
-  const dim3 grid(ncb + (a.map && a.base != a.out ? 1u : 0u), static_cast<unsigned>(g.max_expand));
-  if (a.R <= 16) k_lora_expand<1, true, JMAJOR><<<grid, kBlock, 0, s>>>(a);
-  else if (a.R <= 32) k_lora_expand<1, false, JMAJOR><<<grid, kBlock, 0, s>>>(a);
-  else if (a.R <= 64) k_lora_expand<2, false, JMAJOR><<<grid, kBlock, 0, s>>>(a);
-  else k_lora_expand<4, false, JMAJOR><<<grid, kBlock, 0, s>>>(a);
+  const unsigned ny = static_cast<unsigned>(a.num_tiles < 65528 ? a.num_tiles : 65528);  // dimension limit
+  const unsigned nz = static_cast<unsigned>((a.num_tiles + ny - 1) / ny);
+  const dim3 grid(ncb + (copies(a) ? 1u : 0u), ny, nz);
+  if (a.R <= 16) k_lora_expand<1, true><<<grid, kBlock, 0, s>>>(a);
+  else if (a.R <= 32) k_lora_expand<1, false><<<grid, kBlock, 0, s>>>(a);
+  else if (a.R <= 64) k_lora_expand<2, false><<<grid, kBlock, 0, s>>>(a);
+  else k_lora_expand<4, false><<<grid, kBlock, 0, s>>>(a);
   return hipGetLastError();
 }
 
-template <int JT>
-hipError_t weight_grad(const WeightGradArgs& w, const LoraGeom& g, hipStream_t s) {
-  const unsigned chunks = static_cast<unsigned>(g.max_chunks);
-  const unsigned jg = static_cast<unsigned>((w.R + 16 * JT - 1) / (16 * JT));
-  auto blocks = [&](int nw) {
-    const int per = nw * kCols;
-    return static_cast<unsigned>((w.C[0] + per - 1) / per + (w.C[1] + per - 1) / per);
-  };
+hipError_t launch_gradients(const WeightGradArgs& w, const ExpandArgs& x, const LoraGeom& g, hipStream_t s) {
+  const unsigned wb = static_cast<unsigned>(lora_weight_blocks(g, w.C[0], w.C[1], w.R));
+  const unsigned blocks = wb + static_cast<unsigned>(x.num_tiles * ((x.N + 4 * kCols - 1) / (4 * kCols) + (copies(x) ? 1 : 0)));
   const size_t lds = sizeof(int) << g.chunk_shift;
-  if (g.chunk_waves == 1) k_lora_weight_grad<JT, 1><<<dim3(blocks(1), chunks, jg), kWave, lds, s>>>(w);
-  else k_lora_weight_grad<JT, 2><<<dim3(blocks(2), chunks, jg), 2 * kWave, lds, s>>>(w);
+  const int copy = copies(x) ? 1 : 0;
+  if (w.R <= 16) k_lora_gradients<1, true, 1><<<blocks, kBlock, lds, s>>>(w, x, wb, copy);
+  else if (w.R <= 32) k_lora_gradients<1, false, 2><<<blocks, kBlock, lds, s>>>(w, x, wb, copy);
+  else if (w.R <= 64) k_lora_gradients<2, false, 4><<<blocks, kBlock, lds, s>>>(w, x, wb, copy);
+  else k_lora_gradients<4, false, 4><<<blocks, kBlock, lds, s>>>(w, x, wb, copy);
   return hipGetLastError();
 }
 
@@ -882,7 +951,6 @@ ShrinkArgs shrink_args(const LoraArgs& a, const LoraGeom& g) {
   s.R = a.R;
   s.E = a.E;
   s.stride = g.rows * a.R;
-  s.tiles = a.tiles;
   s.expand_tiles = a.expand_tiles;
   s.num_expand = static_cast<int>(g.max_expand);
   s.expand_shift = g.expand_shift;
@@ -906,6 +974,7 @@ ExpandArgs expand_args(const LoraArgs& a, const LoraGeom& g) {
   x.T = a.T;
   x.R = a.R;
   x.tiles = a.expand_tiles;
+  x.num_tiles = g.max_expand;
   x.status = a.status;
   x.generation = a.generation;
   return x;
@@ -927,7 +996,6 @@ LoraGeom lora_geom(int64_t rows, int E, int H, int N, int R, bool backward) {
   else if (rows < 4096 && tiles > 2) tiles = 2;
   g.row_tiles = static_cast<int>(tiles < wide ? tiles : wide);
   g.max_tiles = up8(rows / (16 * g.row_tiles) + used);
-  g.tile_bytes = static_cast<size_t>(g.max_tiles) * 16;
   // the contraction is split over blocks too until there are two per CU
   auto splits = [&](int C) {
     int n = 1;
@@ -935,6 +1003,8 @@ LoraGeom lora_geom(int64_t rows, int E, int H, int N, int R, bool backward) {
     return n;
   };
   // The result's tiles: the longest that leave about two blocks per CU
+  // (16,384 rows x 4096: 28.0 us with 128 rows, 29.0 with 64, 35.6 with 32;
+  // 8111 x 2048 at rank 64: 35.7 us with 64, 36.6 with 128)
   const int64_t col_blocks = ((backward ? H : N) + 4 * kCols - 1) / (4 * kCols);
   auto expand_tiles = [&](int shift) { return up8((rows >> shift) + used); };
   g.expand_shift = R <= 64 ? 7 : 6;
@@ -950,7 +1020,6 @@ LoraGeom lora_geom(int64_t rows, int E, int H, int N, int R, bool backward) {
     while (g.chunk_shift < 12 && (static_cast<int64_t>(32) << g.chunk_shift) < rows) ++g.chunk_shift;
     g.max_chunks = up8((rows >> g.chunk_shift) + used);
     g.chunk_bytes = static_cast<size_t>(g.max_chunks) * 16;
-    g.chunk_waves = g.max_chunks * ((H + N) / kCols) < 2048 ? 1 : 2;
     // an expert of several chunks has more than one chunk of rows, so its
     // chunks are at most twice its rows over the chunk size
     g.slots = 2 * (rows >> g.chunk_shift);
@@ -959,67 +1028,32 @@ LoraGeom lora_geom(int64_t rows, int E, int H, int N, int R, bool backward) {
   return g;
 }
 
+int64_t lora_weight_blocks(const LoraGeom& g, int H, int N, int R) {
+  const int per = kWavesPerBlock * kCols;
+  const int groups = R <= 64 ? 1 : 2;  // of R
+  return g.max_chunks * groups * ((H + per - 1) / per + (N + per - 1) / per);
+}
+
 hipError_t launch_lora(const LoraArgs& a, const LoraGeom& g, hipStream_t s) {
-  ShrinkArgs sh = shrink_args(a, g);
-  sh.in = a.x;
-  sh.ld = a.ldx;
-  sh.map = a.xmap;
-  sh.w = a.a;
-  sh.C = a.H;
-  sh.part = a.u;
-  sh.S = g.split_x;
-  hipError_t err = shrink<false>(sh, g, s);
+  ShrinkArgs u = shrink_args(a, g);
+  u.in = a.x;
+  u.ld = a.ldx;
+  u.map = a.xmap;
+  u.w = a.a;
+  u.C = a.H;
+  u.part = a.u;
+  u.S = g.split_x;
+  const hipError_t err = launch_shrink(u, nullptr, g, s);
   if (err != hipSuccess) return err;
-  ExpandArgs ex = expand_args(a, g);
-  ex.part = a.u;
-  ex.S = g.split_x;
-  ex.w = a.b;
-  ex.N = a.N;
-  return expand<false>(ex, g, s);
+  ExpandArgs x = expand_args(a, g);
+  x.part = a.u;
+  x.S = g.split_x;
+  x.w = a.b;
+  x.N = a.N;
+  return launch_expand(x, s);
 }
-
-namespace {
-
-// u, v and from v the rows' gradients.
-hipError_t row_gradients(const LoraArgs& a, const LoraGeom& g, hipStream_t s) {
-  ShrinkArgs sh = shrink_args(a, g);
-  sh.in = a.x;
-  sh.ld = a.ldx;
-  sh.map = a.xmap;
-  sh.w = a.a;
-  sh.C = a.H;
-  sh.part = a.u;
-  sh.S = g.split_x;
-  sh.chunks = a.chunks;
-  sh.num_chunks = static_cast<int>(g.max_chunks);
-  sh.chunk_shift = g.chunk_shift;
-  hipError_t err = shrink<false>(sh, g, s);
-  if (err != hipSuccess) return err;
-  sh.known = true;
-  sh.in = a.go;
-  sh.ld = a.ldgo;
-  sh.map = a.omap;
-  sh.w = a.b;
-  sh.C = a.N;
-  sh.part = a.v;
-  sh.S = g.split_g;
-  err = shrink<true>(sh, g, s);
-  if (err != hipSuccess) return err;
-  ExpandArgs ex = expand_args(a, g);
-  ex.part = a.v;
-  ex.S = g.split_g;
-  ex.w = a.a;
-  ex.N = a.H;
-  return expand<true>(ex, g, s);
-}
-
-}  // namespace
 
 hipError_t launch_lora_backward(const LoraArgs& a, const LoraGeom& g, hipStream_t s) {
-  if (g.rows > 0) {
-    const hipError_t err = row_gradients(a, g, s);
-    if (err != hipSuccess) return err;
-  }
   WeightGradArgs w = {};
   w.in[0] = a.x;
   w.ld[0] = a.ldx;
@@ -1046,15 +1080,39 @@ hipError_t launch_lora_backward(const LoraArgs& a, const LoraGeom& g, hipStream_
   w.counts = a.counts;
   w.status = a.status;
   w.generation = a.generation;
-  if (g.rows > 0) {
-    hipError_t err;
-    if (a.R <= 16) err = weight_grad<1>(w, g, s);
-    else if (a.R <= 32) err = weight_grad<2>(w, g, s);
-    else err = weight_grad<4>(w, g, s);
+  if (a.T > 0) {
+    ShrinkArgs u = shrink_args(a, g);
+    ShrinkArgs v = u;
+    u.in = a.x;
+    u.ld = a.ldx;
+    u.map = a.xmap;
+    u.w = a.a;
+    u.C = a.H;
+    u.part = a.u;
+    u.S = g.split_x;
+    u.chunks = a.chunks;
+    u.num_chunks = static_cast<int>(g.max_chunks);
+    u.chunk_shift = g.chunk_shift;
+    v.in = a.go;
+    v.ld = a.ldgo;
+    v.map = a.omap;
+    v.w = a.b;
+    v.C = a.N;
+    v.part = a.v;
+    v.S = g.split_g;
+    v.num_expand = 0;  // u's blocks write the tables
+    hipError_t err = launch_shrink(u, &v, g, s);
+    if (err != hipSuccess) return err;
+    ExpandArgs x = expand_args(a, g);
+    x.part = a.v;
+    x.S = g.split_g;
+    x.w = a.a;
+    x.N = a.H;
+    err = launch_gradients(w, x, g, s);
     if (err != hipSuccess) return err;
   }
-  const int64_t parts = (w.slot_size / 4 + kBlock - 1) / kBlock * a.E;
-  k_lora_join<<<static_cast<unsigned>(parts < 1024 ? parts : 1024), kBlock, 0, s>>>(w);
+  const int64_t parts = (w.slot_size / 4 + kBlock - 1) / kBlock;
+  k_lora_join<<<dim3(static_cast<unsigned>(parts < 256 ? parts : 256), a.E < 8 ? a.E : 8), kBlock, 0, s>>>(w);
   return hipGetLastError();
 }
 

@@ -5,38 +5,102 @@ manner of the package's other entry points; the formulas stand there.
 All tensors of a call must be on one device; the work is enqueued on that
 device's current stream.  The gradients are entry points of their own: call
 them from a ``torch.autograd.Function`` or a hand-written backward pass.
+
+Single tokens are decoded through these calls, so the host's part counts: the
+constant structs of a shape are kept (``functools.lru_cache``), and a tensor
+that is as it should be passes its checks in one expression.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 
 import torch
 
-from . import Layout, _dev, _lib, _problem, _ptr, _resolve, _stream
+from . import Layout, _dev, _lib, _ptr, _resolve
 
-_HERE = contextlib.nullcontext()
-_LOGITS = {torch.float32: _lib.EP_LOGITS_FP32, torch.bfloat16: _lib.EP_LOGITS_BF16}
-
-
-def _on_device(device: torch.device, *others: torch.Tensor | None):
-    """Run on `device`: the library launches on the current device."""
-    for t in others:
-        if t is not None and t.device != device:
-            raise ValueError(f"all tensors must be on {device}, got one on {t.device}")
-    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+_BF16, _F32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int64, torch.uint8
+_LOGITS = {_F32: _lib.EP_LOGITS_FP32, _BF16: _lib.EP_LOGITS_BF16}
 
 
-def _router(logits, topk, score, renormalize, scale, num_groups=0, topk_groups=0, group_top=1) -> _lib.Router:
+def _check(t: torch.Tensor, name: str, dtype: torch.dtype, shape, index: int) -> torch.Tensor:
+    """`t` if it is a contiguous tensor of this type and shape (None: any) on
+    GPU `index`; raises otherwise."""
+    if not (
+        isinstance(t, torch.Tensor)
+        and t.dtype is dtype
+        and t.is_cuda
+        and t.is_contiguous()
+        and (shape is None or t.shape == shape)
+        and t.get_device() == index
+    ):
+        _dev(t, name, dtype, shape)
+        raise ValueError(f"{name} must be on cuda:{index}, as the call's other tensors, got {t.device}")
+    return t
+
+
+def _rows(t: torch.Tensor, name: str, width: int, rows: int, index: int) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, >= {width}]")
+    _check(t, name, _BF16, None, index)
+    have = t.shape
+    if have[1] < width or have[0] < rows:
+        raise ValueError(f"{name} must be at least [{rows}, {width}], got {tuple(have)}")
+    return t
+
+
+def _call(fn: str, index: int, *args) -> None:
+    """The library's `fn` on GPU `index` and its current stream: the library
+    launches on the current device."""
+    if torch.cuda.current_device() == index:
+        rc = getattr(_lib.lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = getattr(_lib.lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc != _lib.EP_OK:
+        _lib.check(fn, rc)
+
+
+@functools.lru_cache(maxsize=1024)
+def _router_struct(*fields):
+    return ctypes.byref(_lib.Router(*fields))
+
+
+@functools.lru_cache(maxsize=1024)
+def _problem_struct(*fields):
+    return ctypes.byref(_lib.Problem(*fields))
+
+
+def _layout_struct(layout: Layout, generation: int) -> _lib.LayoutStruct:
+    """The fields of the C struct that these calls read."""
+    s = _lib.LayoutStruct()
+    s.counts = layout.counts.data_ptr()
+    s.offsets = layout.offsets.data_ptr()
+    s.slot = layout.slot.data_ptr()
+    s.status = layout.status.data_ptr()
+    if layout.expert_row_src is not None:
+        s.expert_row_src = layout.expert_row_src.data_ptr()
+        s.expert_row_capacity = layout.expert_row_capacity
+    s.generation = generation
+    return s
+
+
+def _layout_index(layout: Layout, index: int) -> None:
+    if layout.slot.get_device() != index:
+        raise ValueError(f"layout must be on cuda:{index}, as the call's tensors, got {layout.slot.device}")
+
+
+def _logits(logits: torch.Tensor):
+    """(T, E, EP_LOGITS_*, GPU) of a call's logits."""
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be a [T, E] tensor")
-    if logits.dtype not in _LOGITS:
+    kind = _LOGITS.get(logits.dtype)
+    if kind is None:
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
-    _dev(logits, "logits", logits.dtype)
+    index = logits.get_device() if logits.is_cuda else -1
+    _check(logits, "logits", logits.dtype, None, index)
     T, E = logits.shape
-    return _lib.Router(T, E, int(topk), int(score), _LOGITS[logits.dtype], int(num_groups), int(topk_groups),
-                       int(group_top), int(bool(renormalize)), float(scale))
+    return T, E, kind, index
 
 
 def ep_route(
@@ -65,27 +129,26 @@ def ep_route(
     logit takes an expert out; ``token_mask`` (bool or uint8 [T]) False takes
     a token out; entries without an expert are -1 with weight 0.  ``out`` is
     a pair of tensors to write to."""
-    r = _router(logits, topk, score, renormalize, scale, num_groups, topk_groups, group_top)
-    T, E, K = logits.shape[0], logits.shape[1], int(topk)
-    if bias is not None:
-        _dev(bias, "bias", torch.float32, (E,))
-    if token_mask is not None:
-        if token_mask.dtype not in (torch.bool, torch.uint8):
-            raise TypeError("token_mask must be bool or uint8")
-        _dev(token_mask, "token_mask", token_mask.dtype, (T,))
+    T, E, kind, index = _logits(logits)
+    K = int(topk)
     if K < 1:
         raise ValueError("topk must be at least 1")
+    r = _router_struct(T, E, K, int(score), kind, int(num_groups), int(topk_groups), int(group_top),
+                       int(bool(renormalize)), float(scale))
+    if bias is not None:
+        _check(bias, "bias", _F32, (E,), index)
+    if token_mask is not None:
+        if token_mask.dtype not in (torch.bool, _U8):
+            raise TypeError("token_mask must be bool or uint8")
+        _check(token_mask, "token_mask", token_mask.dtype, (T,), index)
     if out is None:
-        idx = torch.empty(T, K, dtype=torch.int64, device=logits.device)
-        w = torch.empty(T, K, dtype=torch.float32, device=logits.device)
+        idx = torch.empty((T, K), dtype=_I64, device=logits.device)
+        w = torch.empty((T, K), dtype=_F32, device=logits.device)
     else:
         idx, w = out
-        _dev(idx, "out[0]", torch.int64, (T, K))
-        _dev(w, "out[1]", torch.float32, (T, K))
-    with _on_device(logits.device, bias, token_mask, idx, w):
-        rc = _lib.lib().ep_route(ctypes.byref(r), _ptr(logits), _ptr(bias), _ptr(token_mask), _ptr(idx), _ptr(w),
-                                 _stream(logits.device))
-    _lib.check("ep_route", rc)
+        _check(idx, "out[0]", _I64, (T, K), index)
+        _check(w, "out[1]", _F32, (T, K), index)
+    _call("ep_route", index, r, logits.data_ptr(), _ptr(bias), _ptr(token_mask), idx.data_ptr(), w.data_ptr())
     return idx, w
 
 
@@ -104,19 +167,17 @@ def ep_route_backward(
     renormalize and scale.  Returns [T, E] in the logits' type."""
     if not isinstance(topk_idx, torch.Tensor) or topk_idx.dim() != 2:
         raise ValueError("topk_idx must be [T, K]")
+    T, E, kind, index = _logits(logits)
     K = topk_idx.shape[1]
-    r = _router(logits, K, score, renormalize, scale)
-    T = logits.shape[0]
-    _dev(topk_idx, "topk_idx", torch.int64, (T, K))
-    _dev(grad_weights, "grad_weights", torch.float32, (T, K))
+    r = _router_struct(T, E, K, int(score), kind, 0, 0, 1, int(bool(renormalize)), float(scale))
+    _check(topk_idx, "topk_idx", _I64, (T, K), index)
+    _check(grad_weights, "grad_weights", _F32, (T, K), index)
     if out is None:
         out = torch.empty_like(logits)
     else:
-        _dev(out, "out", logits.dtype, logits.shape)
-    with _on_device(logits.device, topk_idx, grad_weights, out):
-        rc = _lib.lib().ep_route_backward(ctypes.byref(r), _ptr(logits), _ptr(topk_idx), _ptr(grad_weights),
-                                          _ptr(out), _stream(logits.device))
-    _lib.check("ep_route_backward", rc)
+        _check(out, "out", logits.dtype, (T, E), index)
+    _call("ep_route_backward", index, r, logits.data_ptr(), topk_idx.data_ptr(), grad_weights.data_ptr(),
+          out.data_ptr())
     return out
 
 
@@ -137,33 +198,33 @@ def ep_combine_backward(
     layout, gen = _resolve(layout)
     if not isinstance(y, torch.Tensor) or y.dim() != 2:
         raise ValueError("y must be [rows, H]")
-    _dev(y, "y", torch.bfloat16)
-    T, K, H = layout.num_tokens, layout.topk, y.shape[1]
-    _dev(grad_out, "grad_out", torch.bfloat16, (T, H))
-    _dev(topk_weights, "topk_weights", torch.float32, (T, K))
+    index = y.get_device() if y.is_cuda else -1
+    _check(y, "y", _BF16, None, index)
+    T, K = layout.num_tokens, layout.topk
+    rows, H = y.shape
+    _check(grad_out, "grad_out", _BF16, (T, H), index)
+    _check(topk_weights, "topk_weights", _F32, (T, K), index)
     if grad_y is None:
         grad_y = torch.empty_like(y)
     else:
-        _dev(grad_y, "grad_y", torch.bfloat16, y.shape)
+        _check(grad_y, "grad_y", _BF16, (rows, H), index)
     if grad_weights is None:
-        grad_weights = torch.empty(T, K, dtype=torch.float32, device=y.device)
+        grad_weights = torch.empty((T, K), dtype=_F32, device=y.device)
     else:
-        _dev(grad_weights, "grad_weights", torch.float32, (T, K))
-    p = _problem(T, H, K, layout.num_experts, layout.num_groups, layout.expert_alignment)
-    s = layout.struct(gen)
-    with _on_device(y.device, grad_out, topk_weights, grad_y, grad_weights, layout.slot):
-        rc = _lib.lib().ep_combine_backward(ctypes.byref(p), ctypes.byref(s), _ptr(topk_weights), _ptr(grad_out),
-                                            _ptr(y), int(y.shape[0]), _ptr(grad_y), _ptr(grad_weights),
-                                            _stream(y.device))
-    _lib.check("ep_combine_backward", rc)
+        _check(grad_weights, "grad_weights", _F32, (T, K), index)
+    _layout_index(layout, index)
+    p = _problem_struct(T, H, K, layout.num_experts, layout.num_groups, layout.expert_alignment, 0)
+    s = _layout_struct(layout, gen)
+    _call("ep_combine_backward", index, p, ctypes.byref(s), topk_weights.data_ptr(), grad_out.data_ptr(),
+          y.data_ptr(), rows, grad_y.data_ptr(), grad_weights.data_ptr())
     return grad_y, grad_weights
 
 
-@functools.lru_cache(maxsize=256)
+@functools.lru_cache(maxsize=1024)
 def _lora_workspace(T, H, K, E, G, A, flags, R, N, wflags, backward) -> int:
-    p = _problem(T, H, K, E, G, A, flags)
     w = _lib.LoraWeights(None, None, None, R, N, wflags)
-    return int(_lib.lib().ep_lora_workspace_bytes(ctypes.byref(p), ctypes.byref(w), backward))
+    return int(_lib.lib().ep_lora_workspace_bytes(_problem_struct(T, H, K, E, G, A, flags), ctypes.byref(w),
+                                                  backward))
 
 
 def ep_lora_workspace_bytes(layout: Layout, hidden: int, n_out: int, rank: int, backward: bool = False) -> int:
@@ -174,49 +235,38 @@ def ep_lora_workspace_bytes(layout: Layout, hidden: int, n_out: int, rank: int, 
                            layout.expert_alignment, 0, int(rank), int(n_out), 0, int(backward))
 
 
-def _rows(t, name, width, rows):
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise ValueError(f"{name} must be [rows, >= {width}]")
-    _dev(t, name, torch.bfloat16)
-    if t.shape[1] < width or t.shape[0] < rows:
-        raise ValueError(f"{name} must be at least [{rows}, {width}], got {tuple(t.shape)}")
-    return t
-
-
-def _adapters(layout, a, b, scales, gather, scatter):
-    """Checks of a call's adapters and row modes; (E, R, N, H, rows of x, rows of out)."""
-    for name, t in (("a", a), ("b", b)):
+def _lora_args(layout, gen, a, b, scales, gather, scatter, backward, workspace):
+    """Checks of a call's adapters, row modes and workspace, and its structs:
+    (R, N, H, rows of x, rows of out, GPU, problem, layout, adapters, workspace)."""
+    for t in (a, b):
         if not isinstance(t, torch.Tensor) or t.dim() != 3:
             raise ValueError("a must be [E, R, H] and b [E, N, R]")
-        _dev(t, name, torch.bfloat16)
+    index = a.get_device() if a.is_cuda else -1
+    _check(a, "a", _BF16, None, index)
     E, R, H = a.shape
     N = b.shape[1]
     if E != layout.num_experts:
         raise ValueError("a must hold one [R, H] matrix per expert of the layout")
-    _dev(b, "b", torch.bfloat16, (E, N, R))
+    _check(b, "b", _BF16, (E, N, R), index)
     if scales is not None:
-        _dev(scales, "scales", torch.float32, (E,))
-    rows = layout.max_expert_rows()
+        _check(scales, "scales", _F32, (E,), index)
+    _layout_index(layout, index)
+    rows, T = layout.max_expert_rows(), layout.num_tokens
     if (gather or scatter) and (layout.expert_row_src is None or layout.expert_row_capacity < rows):
         raise ValueError("gather and scatter need a layout computed with expert_row_src=True")
     if scatter and layout.topk != 1:
         raise ValueError("scatter needs a layout with one selection per token")
-    T = layout.num_tokens
-    return E, R, N, H, T if gather else rows, T if scatter else rows
-
-
-def _lora_structs(layout, gen, a, b, scales, R, N, H, gather, scatter, backward, workspace):
-    flags = _lib.EP_FLAG_GATHER_ROWS if gather else 0
     wflags = _lib.EP_LORA_SCATTER_ROWS if scatter else 0
-    shape = (layout.num_tokens, H, layout.topk, layout.num_experts, layout.num_groups, layout.expert_alignment)
-    p = _problem(*shape, flags)
-    w = _lib.LoraWeights(_ptr(a), _ptr(b), _ptr(scales), R, N, wflags)
-    need = _lora_workspace(*shape, flags, R, N, wflags, int(backward))
+    shape = (T, H, layout.topk, E, layout.num_groups, layout.expert_alignment,
+             _lib.EP_FLAG_GATHER_ROWS if gather else 0)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=a.device)
+        need = _lora_workspace(*shape, R, N, wflags, backward)
+        workspace = torch.empty(need, dtype=_U8, device=a.device)
     else:
-        _dev(workspace, "workspace", torch.uint8)
-    return p, layout.struct(gen), w, workspace
+        _check(workspace, "workspace", _U8, None, index)
+    w = _lib.LoraWeights(a.data_ptr(), b.data_ptr(), _ptr(scales), R, N, wflags)
+    return (R, N, H, T if gather else rows, T if scatter else rows, index, _problem_struct(*shape),
+            ctypes.byref(_layout_struct(layout, gen)), ctypes.byref(w), workspace)
 
 
 def ep_lora(
@@ -246,22 +296,17 @@ def ep_lora(
     ``workspace`` (uint8, ``ep_lora_workspace_bytes``) is allocated if not
     given; calls that may overlap need their own."""
     layout, gen = _resolve(layout)
-    E, R, N, H, xrows, orows = _adapters(layout, a, b, scales, gather, scatter)
-    _rows(x, "x", H, xrows)
+    R, N, H, xrows, orows, index, p, s, w, workspace = _lora_args(layout, gen, a, b, scales, gather, scatter, 0,
+                                                                  workspace)
+    _rows(x, "x", H, xrows, index)
     if base is not None:
-        _rows(base, "base", N, orows)
+        _rows(base, "base", N, orows, index)
     if out is None:
-        out = torch.empty(orows, N, dtype=torch.bfloat16, device=x.device)
+        out = torch.empty((orows, N), dtype=_BF16, device=x.device)
     else:
-        _rows(out, "out", N, orows)
-    with _on_device(x.device, a, b, base, scales, out, workspace, layout.slot):
-        p, s, w, workspace = _lora_structs(layout, gen, a, b, scales, R, N, H, gather, scatter, False, workspace)
-        rc = _lib.lib().ep_lora(
-            ctypes.byref(p), ctypes.byref(s), ctypes.byref(w), _ptr(x), x.shape[1], _ptr(base),
-            0 if base is None else base.shape[1], _ptr(out), out.shape[1], _ptr(workspace), workspace.numel(),
-            _stream(x.device),
-        )
-    _lib.check("ep_lora", rc)
+        _rows(out, "out", N, orows, index)
+    _call("ep_lora", index, p, s, w, x.data_ptr(), x.shape[1], _ptr(base), 0 if base is None else base.shape[1],
+          out.data_ptr(), out.shape[1], workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -292,29 +337,25 @@ def ep_lora_backward(
     without rows gets zero gradients.  The gradient of base is grad_out
     itself."""
     layout, gen = _resolve(layout)
-    E, R, N, H, xrows, orows = _adapters(layout, a, b, scales, gather, scatter)
-    _rows(x, "x", H, xrows)
-    _rows(grad_out, "grad_out", N, orows)
+    R, N, H, xrows, orows, index, p, s, w, workspace = _lora_args(layout, gen, a, b, scales, gather, scatter, 1,
+                                                                  workspace)
+    _rows(x, "x", H, xrows, index)
+    _rows(grad_out, "grad_out", N, orows, index)
     if grad_base is not None:
-        _rows(grad_base, "grad_base", H, orows)
+        _rows(grad_base, "grad_base", H, orows, index)
     if grad_x is None:
-        grad_x = torch.empty(orows, H, dtype=torch.bfloat16, device=x.device)
+        grad_x = torch.empty((orows, H), dtype=_BF16, device=x.device)
     else:
-        _rows(grad_x, "grad_x", H, orows)
+        _rows(grad_x, "grad_x", H, orows, index)
     if grad_a is None:
         grad_a = torch.empty_like(a)
     else:
-        _dev(grad_a, "grad_a", torch.bfloat16, a.shape)
+        _check(grad_a, "grad_a", _BF16, a.shape, index)
     if grad_b is None:
         grad_b = torch.empty_like(b)
     else:
-        _dev(grad_b, "grad_b", torch.bfloat16, b.shape)
-    with _on_device(x.device, a, b, scales, grad_out, grad_base, grad_x, grad_a, grad_b, workspace, layout.slot):
-        p, s, w, workspace = _lora_structs(layout, gen, a, b, scales, R, N, H, gather, scatter, True, workspace)
-        rc = _lib.lib().ep_lora_backward(
-            ctypes.byref(p), ctypes.byref(s), ctypes.byref(w), _ptr(grad_out), grad_out.shape[1], _ptr(x),
-            x.shape[1], _ptr(grad_base), 0 if grad_base is None else grad_base.shape[1], _ptr(grad_x),
-            grad_x.shape[1], _ptr(grad_a), _ptr(grad_b), _ptr(workspace), workspace.numel(), _stream(x.device),
-        )
-    _lib.check("ep_lora_backward", rc)
+        _check(grad_b, "grad_b", _BF16, b.shape, index)
+    _call("ep_lora_backward", index, p, s, w, grad_out.data_ptr(), grad_out.shape[1], x.data_ptr(), x.shape[1],
+          _ptr(grad_base), 0 if grad_base is None else grad_base.shape[1], grad_x.data_ptr(), grad_x.shape[1],
+          grad_a.data_ptr(), grad_b.data_ptr(), workspace.data_ptr(), workspace.numel())
     return grad_x, grad_a, grad_b

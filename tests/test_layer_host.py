@@ -226,8 +226,8 @@ def test_workspace_covers_every_split_of_the_rows():
         E, rows = rng.randint(1, 40), rng.randint(1, 5000)
         cuts = sorted(rng.randint(0, rows) for _ in range(E - 1))
         counts = [b - a for a, b in zip([0, *cuts], [*cuts, rows])]
-        shift = 6
-        while (32 << shift) < rows:
+        shift = 7
+        while shift < 12 and (32 << shift) < rows:
             shift += 1
         chunks = [(c + (1 << shift) - 1) >> shift for c in counts]
         assert sum(c for c in chunks if c > 1) <= 2 * (rows >> shift)
