@@ -44,6 +44,7 @@ int check_router(const ep_router_t* r, bool groups) {
   if (r->logits != EP_LOGITS_FP32 && r->logits != EP_LOGITS_BF16) return EP_EINVAL;
   if ((r->renormalize != 0 && r->renormalize != 1) || !isfinite(r->scale)) return EP_EINVAL;
   if (r->topk > EP_MAX_TOPK || r->num_experts > EP_MAX_KEYS) return EP_ENOTSUP;
+  if (r->num_tokens > INT32_MAX / r->topk) return EP_ENOTSUP;  // what ep_layout takes
   if (groups && r->num_groups != 0) {
     if (r->num_groups < 0 || r->num_experts % r->num_groups != 0) return EP_EINVAL;
     if (r->topk_groups < 1 || r->topk_groups > r->num_groups) return EP_EINVAL;

@@ -28,7 +28,7 @@ extern "C" {
 #define EP_LOGITS_BF16 1
 
 /* A router.
- *   num_tokens   T >= 0
+ *   num_tokens   T >= 0, T * K < 2^31
  *   num_experts  E in [1, EP_MAX_KEYS]
  *   topk         K in [1, EP_MAX_TOPK], K <= E
  *   score, logits  EP_SCORE_*, EP_LOGITS_*

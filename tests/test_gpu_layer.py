@@ -82,6 +82,25 @@ def test_combine_backward_full_size_sampled():
     assert (np.abs(f64(gw[t]) - want_w) <= bound).all()
 
 
+def test_combine_backward_offsets_past_32_bits():
+    """80,000 expert rows x 32,768 (5.2 GB): the last tokens as in a call on
+    rows of their own."""
+    m = ep()
+    T, H = 80_000, 32_768
+    idx = torch.zeros(T, 1, dtype=torch.int64, device=DEV)
+    L = m.ep_layout(idx, 1)
+    wt = torch.full((T, 1), 0.5, device=DEV)
+    go = torch.zeros(T, H, dtype=torch.bfloat16, device=DEV)
+    y = torch.zeros(T, H, dtype=torch.bfloat16, device=DEV)
+    w = W.Workload("cb", T=40, H=H, K=1, E=1, seed=2)
+    go[-40:], y[-40:] = W.make_x(w, device=DEV), W.make_y(w, device=DEV)
+    gy, gw = m.ep_combine_backward(go, y, L, wt)
+    L1 = m.ep_layout(idx[-40:], 1)
+    one = m.ep_combine_backward(go[-40:].clone(), y[-40:].clone(), L1, wt[-40:])
+    assert torch.equal(gy[-40:], one[0]) and torch.equal(gw[-40:], one[1])
+    assert (gy[:-40] == 0).all() and (gw[:-40] == 0).all()
+
+
 def test_combine_backward_masked_oob_and_misaligned():
     m = ep()
     w = W.Workload("cb", T=50, H=264, K=4, E=8, seed=5)

@@ -149,6 +149,22 @@ CASES = [
 ]
 
 
+# 2048 rows and more, 32 and more per expert: tiles of 32 and 64 rows, result
+# tiles of 64 and 128 rows, experts of several weight-gradient chunks
+LARGE = [
+    (2100, 1, 8, 136, 264, 16, True, True, 0, 0),
+    (2100, 1, 40, 72, 520, 32, True, True, 0, 8),
+    (4200, 1, 9, 200, 136, 8, True, True, 0, 0),
+    (4200, 1, 5, 1096, 1032, 24, True, True, 0, 0),
+    (2200, 2, 16, 128, 640, 32, False, False, 64, 0),
+    (2200, 2, 30, 328, 512, 64, True, False, 0, 16),
+    (4500, 1, 6, 264, 200, 128, True, True, 0, 0),
+    (4500, 1, 20, 64, 1160, 112, True, True, 0, 0),
+    (1500, 4, 5, 520, 72, 48, False, False, 0, 0),
+]
+CASES = CASES + LARGE
+
+
 @pytest.mark.parametrize("T,K,E,H,N,R,gather,scatter,A,pad", CASES)
 def test_lora(T, K, E, H, N, R, gather, scatter, A, pad):
     print(f"lora T={T} K={K} E={E} H={H} N={N} R={R} gather={gather} scatter={scatter} A={A} pad={pad}", flush=True)
@@ -166,14 +182,15 @@ def test_lora_backward(T, K, E, H, N, R, gather, scatter, A, pad):
     c.backward(base=True)
 
 
-@pytest.mark.parametrize("gather,scatter,K", [(True, True, 1), (False, False, 2)])
+@pytest.mark.parametrize("gather,scatter,K,T", [(True, True, 1, 150), (False, False, 2, 150), (True, True, 1, 2500),
+                                                (True, False, 2, 2500)])
 @pytest.mark.parametrize("R", [8, 16, 32, 72, 128])
-def test_lora_exact_on_small_integers(R, gather, scatter, K):
+def test_lora_exact_on_small_integers(R, gather, scatter, K, T):
     """Integers in [-2, 2] and a scale of one half: u and v have at most 16
     significand bits (|u| <= 4 H = 2^13 and |v| <= 4 N < 2^13) and every fp32
     sum is exact (below 2^24 in units of one half), so each result is the
     bf16 rounding of the exact value: any misplaced row, column or rank shows."""
-    H, N, T = 2048, 904, 150
+    H, N = 2048, 904
     c = Case(_ids(T, K, 5, R), 5, H, N, R, gather, scatter, seed=R, ints=True)
     got, want = c.forward()
     sel = torch.from_numpy(c.selected)
@@ -234,6 +251,37 @@ def test_lora_infinities_stay_in_their_rows():
     x[7], x[20] = 3e38, 0.0
     got = m.ep_lora(x, c.L, a, b, gather=True, scatter=True)
     assert torch.isposinf(got[7]).all() and (got[20] == 0).all()
+
+
+def test_lora_offsets_past_32_bits():
+    """70,000 token rows 32,768 elements apart (4.6 GB): the last requests as
+    in a call on compact rows."""
+    m = ep()
+    T, E, H, N, R, W = 70_000, 3, 128, 136, 16, 32_768
+    ids = torch.full((T, 1), -1, device=DEV)
+    ids[-500:] = _ids(500, 1, E, 5).to(DEV)
+    small = Case(ids[-500:].cpu(), E, H, N, R, True, True, seed=9)
+    d = small.dev
+    go, xs = d["go"].nan_to_num(0.0, posinf=0.0), d["x"].nan_to_num(0.0)
+    L = m.ep_layout(ids, E, expert_row_src=True)
+    big = torch.zeros(T, W, dtype=torch.bfloat16, device=DEV)
+    big[-500:, :H] = xs
+    base = torch.zeros(T, W, dtype=torch.bfloat16, device=DEV)
+    base[-500:, :N] = d["base"]
+    m.ep_lora(big, L, d["a"], d["b"], base=base, out=base, **small.kw)
+    want = m.ep_lora(xs, small.L, d["a"], d["b"], base=d["base"], **small.kw)
+
+    def close(got, want):
+        # the two calls may split a contraction differently: each result is
+        # within half a bf16 step of nearly the same value, one step in all
+        got, want = got.double(), want.double()
+        return ((got - want).abs() <= 2 * LO.UBF * want.abs() + 1e-3).all()
+
+    assert close(base[-500:, :N], want) and (base[:-500] == 0).all()
+    base[-500:, :N] = go
+    gx, ga, gb = m.ep_lora_backward(base, big, L, d["a"], d["b"], **small.kw)
+    want = m.ep_lora_backward(go, xs, small.L, d["a"], d["b"], **small.kw)
+    assert close(gx[-500:], want[0]) and close(ga, want[1]) and close(gb, want[2]) and (gx[:-500] == 0).all()
 
 
 def test_lora_refuses_and_stale():

@@ -41,13 +41,26 @@ def _bias(E, seed, steps=True):
     return (b * 1000).round() / 1000 if steps else b
 
 
-def _check(l, K, score="softmax", bias=None, G=0, TG=0, gtop=1, renorm=False, scale=1.0, mask=None):
-    print(f"route {tuple(l.shape)} {l.dtype} K={K} {score} bias={bias is not None} G={G}/{TG} top{gtop} "
+def _check(l, K, score="softmax", bias=None, G=0, TG=0, gtop=1, renorm=False, scale=1.0, mask=None, copies=1):
+    """One call on `copies` repetitions of the tokens l against the oracle on l."""
+    print(f"route {copies} x {tuple(l.shape)} {l.dtype} K={K} {score} bias={bias is not None} G={G}/{TG} top{gtop} "
           f"renorm={renorm}", flush=True)
     dev = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    if copies > 1:
+        big = [None if t is None else t.to(DEV).repeat(copies, *[1] * (t.dim() - 1)) for t in (l, mask)]
+        idx, w = ep().ep_route(big[0], K, score=_score(score), bias=dev(bias), num_groups=G, topk_groups=TG,
+                               group_top=gtop, renormalize=renorm, scale=scale, token_mask=big[1])
+        one = idx[: len(l)].repeat(copies, 1), w[: len(l)].repeat(copies, 1)
+        assert torch.equal(idx, one[0]) and torch.equal(w, one[1])
+        idx, w = idx[: len(l)], w[: len(l)]
+        return _compare(l, K, score, bias, G, TG, gtop, renorm, scale, mask, idx, w)
     idx, w = ep().ep_route(dev(l), K, score=_score(score), bias=dev(bias), num_groups=G, topk_groups=TG,
                            group_top=gtop, renormalize=renorm, scale=scale, token_mask=dev(mask))
     torch.cuda.synchronize()
+    return _compare(l, K, score, bias, G, TG, gtop, renorm, scale, mask, idx, w)
+
+
+def _compare(l, K, score, bias, G, TG, gtop, renorm, scale, mask, idx, w):
     l64 = l.double().numpy()
     want_i, want_w = LO.route(l64, K, score, None if bias is None else bias.double().numpy(), G, TG, gtop, renorm, scale,
                               None if mask is None else mask.numpy())
@@ -76,6 +89,30 @@ def test_route_shapes(T, E, K, dtype):
     _check(l, K, "sigmoid", bias=_bias(E, T), renorm=True)
     _check(l, K, "softmax", bias=_bias(E, T, steps=False) * 0.1)
     _check(l, K, "sigmoid")
+
+
+# more than 2048 tokens: 16, 32 or 64 lanes a token, 4 to 16 values a lane, all or half of them kept
+BIG = [(3, 1, 1), (37, 7, 3), (33, 64, 32), (21, 100, 9), (41, 128, 8), (35, 129, 8), (29, 256, 8), (13, 256, 17),
+       (27, 255, 8), (19, 300, 8), (11, 512, 32), (17, 512, 5), (9, 1024, 8), (7, 1000, 32)]
+
+
+@pytest.mark.parametrize("T,E,K", BIG)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_large_batches(T, E, K, dtype):
+    l = _logits(T, E, dtype, T * 7 + E)
+    copies = 2100 // T + 1
+    _check(l, K, renorm=True, scale=2.5, copies=copies)
+    _check(l, K, "softmax", copies=copies)
+    _check(l, K, "sigmoid", bias=_bias(E, T), copies=copies)
+    _check(l, K, "softmax", bias=_bias(E, T, steps=False) * 0.1, renorm=True, copies=copies)
+    if E % 4 == 0:
+        G = 4 if E <= 512 else 8
+        TG = next(n for n in range(1, G + 1) if n * E // G >= K)
+        mask = torch.ones(T, dtype=torch.bool)
+        mask[::3] = False
+        _check(l, K, "sigmoid", _bias(E, G), G, TG, 2, True, 2.5, mask, copies=copies)
+        _check(l, K, "softmax", None, G, TG, 2, copies=copies)
+        _check(l, K, "softmax", None, G, TG, 1, mask=mask, copies=copies)
 
 
 @pytest.mark.parametrize("E,G,TG,gtop,K", [(256, 8, 4, 2, 8), (256, 8, 3, 1, 8), (160, 8, 3, 2, 6), (96, 32, 5, 2, 7),
@@ -113,9 +150,10 @@ def test_route_masks_and_special_values(dtype):
     mask[[13, 20, 23]] = False
     for score in ("softmax", "sigmoid"):
         for renorm in (False, True):
-            _check(l, 6, score, renorm=renorm, mask=mask)
-            _check(l, 6, score, bias=_bias(E, 3), renorm=renorm, mask=mask)
-            _check(l, 6, score, bias=torch.zeros(E), G=8, TG=3, gtop=2, renorm=renorm, mask=mask)
+            for n in (1, 90):
+                _check(l, 6, score, renorm=renorm, mask=mask, copies=n)
+                _check(l, 6, score, bias=_bias(E, 3), renorm=renorm, mask=mask, copies=n)
+                _check(l, 6, score, bias=torch.zeros(E), G=8, TG=3, gtop=2, renorm=renorm, mask=mask, copies=n)
     b = _bias(E, 4)
     b[0], b[1], b[2] = nan, -inf, inf
     _check(l[13:], 6, "sigmoid", bias=b)
@@ -142,6 +180,38 @@ def test_route_neighbouring_scores_are_ordered_in_binary64():
     _check(l, 8, "sigmoid", bias=torch.zeros(E), G=8, TG=3, gtop=2)
     p = torch.softmax(l[0].double(), 0)
     _check(l, 8, "softmax", bias=(0.5 - p).float())
+    for n in (8, 32):
+        _check(l, n, "sigmoid", bias=b, renorm=True, copies=70)
+        _check(l, n, "softmax", bias=(0.5 - p).float(), copies=70)
+        _check(l, n, copies=70)  # fp32 logits a step apart
+    _check(l, 8, "sigmoid", bias=b, G=8, TG=3, gtop=2, copies=70)
+    _check(l, 8, "softmax", G=8, TG=3, gtop=2, copies=70)
+
+
+def test_route_all_experts_equal():
+    """Every value equal (a router that starts at zero): more candidates than
+    are kept, ties to the lowest index."""
+    for E in (64, 256, 1024):
+        for copies in (1, 1100):
+            l = torch.zeros(2, E)
+            _check(l, 8, copies=copies)
+            _check(l, 8, "sigmoid", bias=torch.zeros(E), G=4, TG=2, gtop=2, renorm=True, copies=copies)
+
+
+def test_route_offsets_past_32_bits():
+    """9 million tokens x 256 bf16 logits, 4.6 GB: the last tokens as in a call
+    of their own, and the gradient likewise."""
+    m = ep()
+    T, E, K = 9_000_000, 256, 8
+    l = torch.zeros(T, E, dtype=torch.bfloat16, device=DEV)
+    l[-300:] = _logits(300, E, torch.bfloat16, 3).to(DEV)
+    idx, w = m.ep_route(l, K, renormalize=True)
+    one = l[-300:].clone()
+    want = m.ep_route(one, K, renormalize=True)
+    assert torch.equal(idx[-300:], want[0]) and torch.equal(w[-300:], want[1])
+    assert torch.equal(idx[0], torch.arange(K, device=DEV))
+    g = m.ep_route_backward(w, l, idx)
+    assert torch.equal(g[-300:], m.ep_route_backward(want[1], one, want[0]))
 
 
 def test_route_noncontiguous_alignment_and_out():

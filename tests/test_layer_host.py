@@ -61,7 +61,7 @@ def _route(**kw):
     (dict(renorm=2), "EINVAL"), (dict(scale=float("nan")), "EINVAL"), (dict(scale=float("inf")), "EINVAL"),
     (dict(G=7, TG=1), "EINVAL"), (dict(G=-1, TG=1), "EINVAL"), (dict(G=8, TG=0), "EINVAL"),
     (dict(G=8, TG=9), "EINVAL"), (dict(G=8, TG=1, gtop=3), "EINVAL"), (dict(G=32, TG=1, K=4), "EINVAL"),
-    (dict(E=130, G=65, TG=65), "ENOTSUP"),
+    (dict(E=130, G=65, TG=65), "ENOTSUP"), (dict(T=1 << 29), "ENOTSUP"),
 ])
 def test_route_refusals(kw, code):
     r = _route(**kw)
