@@ -428,7 +428,9 @@ __global__ __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) void
     auto expert = [&](int i) { return (i / 4) * 4 * LPT + 4 * g + i % 4; };
     uint32_t all_keys[NV];
     auto make_key = [&](int i, float v) {
-      return v > kNegInf ? (ordered(v) & ~kLowMask) | (kLowMask - static_cast<uint32_t>(BY == kByBf16 ? expert(i) : i)) : 0u;
+      uint32_t key = (ordered(v) & ~kLowMask) | (kLowMask - static_cast<uint32_t>(BY == kByBf16 ? expert(i) : i));
+      asm("" : "+v"(key));  // a select, not a branch around the key's making
+      return v > kNegInf ? key : 0u;
     };
     if constexpr (BY == kByBf16) {
       // NaN is left out by the comparison; +inf stays above the largest bf16
@@ -594,42 +596,46 @@ __global__ __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) void
       return u - v <= tol;
     };
     const uint64_t before = lanemask_lt() & ~((1ull << (tok * LPT)) - 1);  // the token's lanes below this one
-    uint32_t prev = 0;
-    int taken = 0;  // of this lane's keys
+    auto drop_head = [&](bool mine) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < KEEP - 1; ++i) key[i] = mine ? key[i + 1] : key[i];
+      key[KEEP - 1] = mine ? 0u : key[KEEP - 1];
+    };
     int count = 0;  // candidates, in the same order in all of the token's lanes
-    while (!doubt) {
-      const uint32_t m = over_token<LPT>(key[0], Max());
-      if (m == 0u) break;
-      if (count >= K) {
-        if (BY == kByBf16 || !close(prev, m)) break;
-        if (count == kCand) {
-          doubt = true;
-          break;
-        }
+    if constexpr (BY == kByBf16) {
+      for (int k = 0; k < K; ++k) {
+        const uint32_t m = over_token<LPT>(key[0], Max());
+        drop_head(key[0] == m);
+        const int e = m != 0u ? static_cast<int>(kLowMask - (m & kLowMask)) : -1;
+#pragma unroll
+        for (int i = 0; i < kOut; ++i) chosen[i] = k == g + i * LPT ? e : chosen[i];
       }
-      bool mine = key[0] == m;
-      if (BY == kByBf16) {
-        if (mine) idxs[count] = static_cast<int>(kLowMask - (m & kLowMask));
-      } else {
+    } else {
+      int taken = 0;  // of this lane's keys
+      uint32_t prev = 0;
+      for (int k = 0;; ++k) {
+        const uint32_t m = over_token<LPT>(key[0], Max());
+        if (k >= K) {  // beyond the Kth, down to the first clear gap
+          if (prev == 0u || m == 0u || !close(prev, m)) break;
+          if (count == kCand) {
+            doubt = true;
+            break;
+          }
+        }
+        bool mine = key[0] == m && m != 0u;
         mine = mine && (ballot(mine) & before) == 0;  // the lowest lane of equal keys
         if (mine) {
           keys[count] = m;
           idxs[count] = expert(static_cast<int>(kLowMask - (m & kLowMask)));
         }
-      }
-#pragma unroll
-      for (int i = 0; i < KEEP - 1; ++i) key[i] = mine ? key[i + 1] : key[i];
-      key[KEEP - 1] = mine ? 0u : key[KEEP - 1];
-      prev = m;
-      ++count;
-      if (BY == kByBf16) {
-        if (count == K) break;
-      } else if (KEEP < NV) {
+        drop_head(mine);
+        count += m != 0u ? 1 : 0;
         taken += mine ? 1 : 0;
+        prev = m;
       }
+      // a lane whose kept keys are used up may have had another
+      if (KEEP < NV) doubt |= over_token<LPT>(taken == KEEP ? 1u : 0u, Or()) != 0u;
     }
-    // a lane whose kept keys are used up may have had another
-    if (BY != kByBf16 && KEEP < NV) doubt |= over_token<LPT>(taken == KEEP ? 1u : 0u, Or()) != 0u;
     lds_sync();
     bool near = false;  // the candidates were put in order by their exact values: in keys
     if (BY != kByBf16 && !doubt) {
@@ -663,7 +669,7 @@ __global__ __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) void
 #pragma unroll
       for (int i = 0; i < kOut; ++i)
         if (g + i * LPT < K) chosen[i] = idxs[g + i * LPT];
-    } else {
+    } else if (BY != kByBf16) {
 #pragma unroll
       for (int i = 0; i < kOut; ++i) {
         const int k = g + i * LPT;
