@@ -93,7 +93,7 @@ int check_lora(const ep_problem_t* p, const ep_lora_weights_t* w) {
   // grid limits: fewer than 2^32 threads, and 2^31 row indices (check_problem)
   if (static_cast<int64_t>(p->hidden) + w->n_out > (1 << 24)) return EP_ENOTSUP;
   const ep::LoraGeom g = geom_of(p, w, true);
-  const int64_t cols = (p->hidden > w->n_out ? p->hidden : w->n_out) / 512 + 2;
+  const int64_t cols = (p->hidden > w->n_out ? p->hidden : w->n_out) / 512 + 1 + 16;  // and the copies'
   if (g.max_tiles >= (1 << 23) ||
       g.max_expand * cols + ep::lora_weight_blocks(g, p->hidden, w->n_out, w->rank) >= (1 << 24))
     return EP_ENOTSUP;

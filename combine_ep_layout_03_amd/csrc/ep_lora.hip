@@ -36,6 +36,7 @@ namespace {
 constexpr int kCols = 128;  // columns of one wave
 constexpr int kXcds = 8;
 constexpr int kMaxSplits = 4;  // splits of a contraction over blocks
+constexpr int kMaxCopyColumns = 16;
 
 __device__ __forceinline__ f32x4_t mfma(u32x4 a, u32x4 b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
@@ -413,18 +414,32 @@ struct ExpandArgs {
 };
 
 // Rows of out that belong to no selection (token rows only): base's row, or
-// zeros.  A block takes 32 tokens from t0, then from t0 + step, ...
+// zeros.  A block takes 8 tokens from t0, then from t0 + step, ...; requests
+// without an adapter are runs of tokens, so a wave takes no more than two at a
+// time (with eight, 10% of 8111 tokens x 2048 took 36 us, the rest of the kernel 26).
+constexpr int kCopyTokens = 8;
 __device__ __forceinline__ void copy_unselected(const ExpandArgs& a, int64_t t0, int64_t step) {
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+  constexpr int kEach = kCopyTokens / kWavesPerBlock;
   for (; t0 < a.T; t0 += step) {
-    for (int i = 0; i < 8; ++i) {
-      const int64_t t = t0 + wave * 8 + i;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int64_t t = t0 + wave * kEach + i;
       if (t >= a.T || a.slot[t] >= 0) continue;
-      for (int n = lane * 8; n < a.N; n += kWave * 8) {
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (a.base) v = load16(a.base + t * a.ldbase + n);
-        *reinterpret_cast<u32x4*>(a.out + t * a.ldout + n) = v;
+      for (int n0 = lane * 8; n0 < a.N; n0 += 4 * kWave * 8) {
+        u32x4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[k] = u32x4{0u, 0u, 0u, 0u};
+          const int n = n0 + k * kWave * 8;
+          if (a.base && n < a.N) v[k] = load16(a.base + t * a.ldbase + n);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int n = n0 + k * kWave * 8;
+          if (n < a.N) *reinterpret_cast<u32x4*>(a.out + t * a.ldout + n) = v[k];
+        }
       }
     }
   }
@@ -641,8 +656,10 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(KS == 1 
   if (!layout_current(a.status, a.generation)) return;
   const int64_t index = static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y;
   const int ncb = (a.N + 4 * kCols - 1) / (4 * kCols);
-  if (static_cast<int>(blockIdx.x) == ncb) {  // the column of rows of no selection
-    copy_unselected(a, index * 32, static_cast<int64_t>(gridDim.y) * gridDim.z * 32);
+  if (static_cast<int>(blockIdx.x) >= ncb) {  // the columns of rows of no selection
+    const int64_t copies = gridDim.x - ncb;
+    copy_unselected(a, (index * copies + blockIdx.x - ncb) * kCopyTokens,
+                    copies * gridDim.y * gridDim.z * kCopyTokens);
     return;
   }
   expand<KS, PACK, false>(a, index, static_cast<int>(blockIdx.x), s_mem);
@@ -831,7 +848,8 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(2))) voi
     const int cols = ncb + copy;
     const int at = static_cast<int>(blockIdx.x - weight_blocks);
     const int cb = at % cols;
-    if (cb == ncb) copy_unselected(x, static_cast<int64_t>(at / cols) * 32, x.num_tiles * 32);
+    if (cb >= ncb) copy_unselected(x, (static_cast<int64_t>(at / cols) * copy + cb - ncb) * kCopyTokens,
+                                   x.num_tiles * copy * kCopyTokens);
     else expand<KS, PACK, true>(x, at / cols, cb, s_mem);
   }
 }
@@ -917,14 +935,20 @@ hipError_t launch_shrink(const ShrinkArgs& u, const ShrinkArgs* v, const LoraGeo
   return hipGetLastError();
 }
 
-// Is there a row of no selection to write?
-bool copies(const ExpandArgs& a) { return a.map && a.base != a.out; }
+// Columns of blocks that write the rows of no selection, beside the result's:
+// 0 where there are none to write.
+int64_t copy_columns(const ExpandArgs& a) {
+  if (!a.map || a.base == a.out) return 0;
+  const int64_t blocks = (a.T + kCopyTokens - 1) / kCopyTokens;
+  const int64_t n = (blocks + a.num_tiles - 1) / a.num_tiles;
+  return n < kMaxCopyColumns ? n : kMaxCopyColumns;
+}
 
 hipError_t launch_expand(const ExpandArgs& a, hipStream_t s) {
   const unsigned ncb = static_cast<unsigned>((a.N + 4 * kCols - 1) / (4 * kCols));
   const unsigned ny = static_cast<unsigned>(a.num_tiles < 65528 ? a.num_tiles : 65528);  // dimension limit
   const unsigned nz = static_cast<unsigned>((a.num_tiles + ny - 1) / ny);
-  const dim3 grid(ncb + (copies(a) ? 1u : 0u), ny, nz);
+  const dim3 grid(ncb + static_cast<unsigned>(copy_columns(a)), ny, nz);
   if (a.R <= 16) k_lora_expand<1, true><<<grid, kBlock, 0, s>>>(a);
   else if (a.R <= 32) k_lora_expand<1, false><<<grid, kBlock, 0, s>>>(a);
   else if (a.R <= 64) k_lora_expand<2, false><<<grid, kBlock, 0, s>>>(a);
@@ -934,9 +958,9 @@ hipError_t launch_expand(const ExpandArgs& a, hipStream_t s) {
 
 hipError_t launch_gradients(const WeightGradArgs& w, const ExpandArgs& x, const LoraGeom& g, hipStream_t s) {
   const unsigned wb = static_cast<unsigned>(lora_weight_blocks(g, w.C[0], w.C[1], w.R));
-  const unsigned blocks = wb + static_cast<unsigned>(x.num_tiles * ((x.N + 4 * kCols - 1) / (4 * kCols) + (copies(x) ? 1 : 0)));
+  const int copy = static_cast<int>(copy_columns(x));
+  const unsigned blocks = wb + static_cast<unsigned>(x.num_tiles * ((x.N + 4 * kCols - 1) / (4 * kCols) + copy));
   const size_t lds = sizeof(int) << g.chunk_shift;
-  const int copy = copies(x) ? 1 : 0;
   if (w.R <= 16) k_lora_gradients<1, true, 1><<<blocks, kBlock, lds, s>>>(w, x, wb, copy);
   else if (w.R <= 32) k_lora_gradients<1, false, 2><<<blocks, kBlock, lds, s>>>(w, x, wb, copy);
   else if (w.R <= 64) k_lora_gradients<2, false, 4><<<blocks, kBlock, lds, s>>>(w, x, wb, copy);
