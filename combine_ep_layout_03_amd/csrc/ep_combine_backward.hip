@@ -9,7 +9,10 @@
 // grad_out vector once and with it the K rows' vectors, so K loads are in
 // flight, adds to K dot products held in registers and stores K vectors.  The
 // lanes' partial sums are added in a butterfly and the waves' partial sums
-// in ascending order: a fixed order, no atomics.
+// in ascending order: a fixed order, no atomics.  8192 tokens x 7168, top-8 of
+// 256 (2.0 GB): 405 us, 4.9 TB/s, where a plain copy reaches 4.98; 368 us where
+// every token names the same 8 experts, so neighbouring tokens' rows are
+// neighbours.
 #include "ep_layer.h"
 
 namespace ep {
@@ -153,6 +156,10 @@ hipError_t launch_t(const CombineBackwardArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// One wave a token where the row has one vector per lane at most (8193 x 256,
+// top-2: 6.5 us against 11.6 with four waves; 8191 x 512: 9.2 against 13.4),
+// else four (8191 x 2048, top-8: 107 us against 117 with one; 126 tokens: 5.3
+// against 8.1; 8192 x 7168: 405 against 401).
 template <int KMAX, int VE>
 hipError_t launch_w(const CombineBackwardArgs& a, hipStream_t s) {
   return a.H / VE <= kWave ? launch_t<KMAX, VE, 1>(a, s) : launch_t<KMAX, VE, 4>(a, s);
