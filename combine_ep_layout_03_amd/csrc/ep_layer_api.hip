@@ -6,6 +6,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "ep_layer.h"
 
 namespace {
@@ -19,6 +21,21 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
   return a && b && pa < pb + static_cast<uintptr_t>(nb) && pb < pa + static_cast<uintptr_t>(na);
+}
+
+struct Span {
+  const void* p;  // null: not there
+  int64_t n;      // bytes
+};
+// Does an output share a byte with an input or another output?
+bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span* other = outs.begin(); other != o; ++other)
+      if (overlap(o->p, o->n, other->p, other->n)) return true;
+    for (const Span& i : ins)
+      if (overlap(o->p, o->n, i.p, i.n)) return true;
+  }
+  return false;
 }
 
 // The shape checks of ep_mi355x.h's calls, for the fields a call on a
@@ -70,6 +87,12 @@ bool rows_overlap(const Rows& a, const Rows& b) {
   const int64_t d = pb >= pa ? static_cast<int64_t>((pb - pa) % static_cast<uintptr_t>(ld))
                              : (ld - static_cast<int64_t>((pa - pb) % static_cast<uintptr_t>(ld))) % ld;
   return !(d >= a.width && d + b.width <= ld);
+}
+
+bool workspace_overlaps(const void* workspace, size_t bytes, std::initializer_list<Rows> used) {
+  for (const Rows& r : used)
+    if (r.n > 0 && overlap(workspace, static_cast<int64_t>(bytes), r.p, (r.n - 1) * r.ld + r.width)) return true;
+  return false;
 }
 
 int64_t max_rows(const ep_problem_t* p) {
@@ -171,6 +194,10 @@ int ep_route(const ep_router_t* r, const void* logits, const float* bias,
   const int el = r->logits == EP_LOGITS_FP32 ? 4 : 2;
   if (!aligned(logits, el) || !aligned(bias, 4) || !aligned(topk_idx, 8) || !aligned(topk_weights, 4))
     return EP_EINVAL;
+  const int64_t sel = r->num_tokens * r->topk;
+  if (clash({{topk_idx, 8 * sel}, {topk_weights, 4 * sel}},
+            {{logits, r->num_tokens * r->num_experts * el}, {bias, 4LL * r->num_experts}, {token_mask, r->num_tokens}}))
+    return EP_EINVAL;
   ep::RouteArgs a = route_args(r);
   a.logits = logits;
   a.bias = bias;
@@ -195,7 +222,8 @@ int ep_route_backward(const ep_router_t* r, const void* logits, const int64_t* t
       !aligned(grad_weights, 4))
     return EP_EINVAL;
   const int64_t bytes = r->num_tokens * r->num_experts * el;
-  if (overlap(logits, bytes, grad_logits, bytes)) return EP_EINVAL;
+  const int64_t sel = r->num_tokens * r->topk;
+  if (clash({{grad_logits, bytes}}, {{logits, bytes}, {topk_idx, 8 * sel}, {grad_weights, 4 * sel}})) return EP_EINVAL;
   ep::RouteArgs a = route_args(r);
   a.logits = logits;
   a.idx = const_cast<int64_t*>(topk_idx);  // read only
@@ -216,9 +244,9 @@ int ep_combine_backward(const ep_problem_t* p, const ep_layout_t* L, const float
   if (!aligned(grad_out, 2) || !aligned(y, 2) || !aligned(grad_y, 2) || !aligned(topk_weights, 4) ||
       !aligned(grad_weights, 4))
     return EP_EINVAL;
-  const int64_t row_bytes = static_cast<int64_t>(p->hidden) * 2;
-  if (overlap(grad_y, y_rows * row_bytes, y, y_rows * row_bytes) ||
-      overlap(grad_y, y_rows * row_bytes, grad_out, p->num_tokens * row_bytes))
+  const int64_t row_bytes = static_cast<int64_t>(p->hidden) * 2, weights = 4 * p->num_tokens * p->topk;
+  if (clash({{grad_y, y_rows * row_bytes}, {grad_weights, weights}},
+            {{y, y_rows * row_bytes}, {grad_out, p->num_tokens * row_bytes}, {topk_weights, weights}}))
     return EP_EINVAL;
   ep::CombineBackwardArgs a;
   a.go = grad_out;
@@ -269,6 +297,9 @@ int ep_lora(const ep_problem_t* p, const ep_layout_t* L, const ep_lora_weights_t
     return EP_EINVAL;
   if (!workspace || !aligned(workspace, 16)) return EP_EINVAL;
   if (workspace_bytes < g.bytes()) return EP_EWORKSPACE;
+  if (workspace_overlaps(workspace, g.bytes(), {ro, {x, xrows, 2LL * a.H, 2 * a.ldx}, {a.a, 1, na, na}, {a.b, 1, nb, nb},
+                                                {base, base ? orows : 0, 2LL * a.N, 2 * a.ldbase}}))
+    return EP_EINVAL;
   a.x = static_cast<const uint16_t*>(x);
   a.base = static_cast<const uint16_t*>(base);
   a.out = static_cast<uint16_t*>(out);
@@ -320,6 +351,9 @@ int ep_lora_backward(const ep_problem_t* p, const ep_layout_t* L, const ep_lora_
   }
   if (!workspace || !aligned(workspace, 16)) return EP_EINVAL;
   if (workspace_bytes < g.bytes()) return EP_EWORKSPACE;
+  if (workspace_overlaps(workspace, g.bytes(), {outs[0], outs[1], outs[2], ins[0], ins[1], ins[2], ins[3],
+                                                {grad_base, grad_base ? orows : 0, 2LL * a.H, 2 * a.ldbase}}))
+    return EP_EINVAL;
   a.x = static_cast<const uint16_t*>(x);
   a.go = static_cast<const uint16_t*>(grad_out);
   a.base = static_cast<const uint16_t*>(grad_base);

@@ -61,13 +61,22 @@ def _call(fn: str, index: int, *args) -> None:
         _lib.check(fn, rc)
 
 
+def _int32(*values) -> None:
+    """Raises for a value that the C structs' int32 fields would cut."""
+    for v in values:
+        if not -(1 << 31) <= v < 1 << 31:
+            raise ValueError(f"{v} does not fit an int32")
+
+
 @functools.lru_cache(maxsize=1024)
 def _router_struct(*fields):
+    _int32(*fields[1:-1])
     return ctypes.byref(_lib.Router(*fields))
 
 
 @functools.lru_cache(maxsize=1024)
 def _problem_struct(*fields):
+    _int32(*fields[1:])
     return ctypes.byref(_lib.Problem(*fields))
 
 
@@ -222,6 +231,7 @@ def ep_combine_backward(
 
 @functools.lru_cache(maxsize=1024)
 def _lora_workspace(T, H, K, E, G, A, flags, R, N, wflags, backward) -> int:
+    _int32(R, N)
     w = _lib.LoraWeights(None, None, None, R, N, wflags)
     return int(_lib.lib().ep_lora_workspace_bytes(_problem_struct(T, H, K, E, G, A, flags), ctypes.byref(w),
                                                   backward))

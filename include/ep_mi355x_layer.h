@@ -76,7 +76,7 @@ typedef struct ep_router {
  * by the token's sum of chosen scores (formed relative to the largest, so
  * that scores which underflow still share it), in fp32.
  * logits, bias and topk_weights must be aligned to their elements, topk_idx
- * to 8 bytes. */
+ * to 8 bytes; the outputs must overlap neither an input nor each other. */
 int ep_route(const ep_router_t* r, const void* logits, const float* bias,
              const uint8_t* token_mask, int64_t* topk_idx, float* topk_weights,
              hipStream_t stream);
@@ -92,8 +92,8 @@ int ep_route(const ep_router_t* r, const void* logits, const float* bias,
  *   sigmoid, renormalize: w_k * (1 - s_k) * (g_k - sum_j g_j w_j) there, else 0
  * The choice is constant and the bias has no gradient.  Entries of topk_idx
  * outside [0, E) have no part; an expert named twice gets both terms.  Sums
- * are fp32; a bf16 result is rounded once.  r's groups are not used and
- * may be 0. */
+ * are fp32; a bf16 result is rounded once.  grad_logits must not overlap an
+ * input.  r's groups are not used and may be 0. */
 int ep_route_backward(const ep_router_t* r, const void* logits, const int64_t* topk_idx,
                       const float* grad_weights, void* grad_logits, hipStream_t stream);
 
@@ -107,8 +107,8 @@ int ep_route_backward(const ep_router_t* r, const void* logits, const int64_t* t
  * not written.  Both combine orders have this gradient; a bias row's gradient
  * is grad_out itself.  Each product of grad_y is one fp32 rounding before the
  * bf16 one; the sum runs in fp32 in a fixed order, so equal inputs give equal
- * bytes.  grad_y must not overlap y or grad_out.  A stale L writes nothing
- * but EP_STATUS_STALE = 1.
+ * bytes.  The outputs must overlap neither an input nor each other.  A stale L
+ * writes nothing but EP_STATUS_STALE = 1.
  * (The gradient of ep_dispatch is ep_combine with unit weights.) */
 int ep_combine_backward(const ep_problem_t* p, const ep_layout_t* L, const float* topk_weights,
                         const void* grad_out, const void* y, int64_t y_rows, void* grad_y,
@@ -152,12 +152,14 @@ size_t ep_lora_workspace_bytes(const ep_problem_t* p, const ep_lora_weights_t* w
  *   out   bf16, row stride out_row_stride (0 = N)
  * Rows of no selection: with EP_LORA_SCATTER_ROWS they become base's row
  * (zeros without one), so all T rows of out are defined; otherwise they are
- * not written.  out must not overlap x, nor base unless it is base.
+ * not written.  out must not overlap x, nor base unless it is base (token
+ * matrices have T rows, the others are taken to have T * K + E * (A - 1), A the
+ * alignment or 1).
  * Requires H % 8 == 0, row strides multiples of 8, bases 16-byte aligned
  * (EP_ENOTSUP for sizes, EP_EINVAL for strides and bases), and `workspace`
  * of ep_lora_workspace_bytes, 16-byte aligned (contents need no
- * initialisation and are clobbered; calls that may overlap in time need
- * their own).  A stale L writes no row and sets EP_STATUS_STALE. */
+ * initialisation and are clobbered; it must not overlap another argument, and
+ * calls that may overlap in time need their own).  A stale L writes no row and sets EP_STATUS_STALE. */
 int ep_lora(const ep_problem_t* p, const ep_layout_t* L, const ep_lora_weights_t* w, const void* x,
             int64_t x_row_stride, const void* base, int64_t base_row_stride, void* out,
             int64_t out_row_stride, void* workspace, size_t workspace_bytes, hipStream_t stream);

@@ -187,6 +187,45 @@ def test_lora_backward_overlaps_and_workspace():
     assert call(nws=need - 1) == _lib.EP_EWORKSPACE
 
 
+def test_outputs_over_inputs_and_each_other():
+    L, f, r = _lib.lib(), FAR, _route()  # 16 x 64 logits of 4 bytes, 16 x 4 selections
+
+    def at(base, bytes_):
+        return ctypes.c_void_p(base.value + bytes_)
+
+    last = at(f[0], 16 * 64 * 4 - 8)
+    for args in ([f[0], None, None, f[0], f[2]], [f[0], None, None, last, f[2]], [f[0], None, None, f[1], last],
+                 [f[0], f[1], None, f[1], f[2]], [f[0], None, at(f[2], 255), f[1], f[2]],
+                 [f[0], None, None, f[1], at(f[1], 508)]):
+        assert L.ep_route(ctypes.byref(r), *args, None) == _lib.EP_EINVAL, args
+    for args in ([f[0], f[1], f[2], f[1]], [f[0], f[1], f[2], at(f[2], 252)]):
+        assert L.ep_route_backward(ctypes.byref(r), *args, None) == _lib.EP_EINVAL, args
+    lay, p = _layout(), _lib.Problem(16, 256, 4, 64, 0, 0, 0)
+    for w, go, y, gy, gw in ([f[0], f[1], f[2], f[3], f[0]], [f[0], f[1], f[2], f[3], f[1]], [f[0], f[1], f[2], f[3], f[2]],
+                             [f[0], f[1], f[2], f[3], f[3]], [f[0], f[1], f[2], f[0], f[4]]):
+        assert L.ep_combine_backward(ctypes.byref(p), ctypes.byref(lay), w, go, y, 64, gy, gw, None) == _lib.EP_EINVAL
+    p, w = _lib.Problem(16, 256, 1, 64, 0, 0, 0), _weights()
+    need = [L.ep_lora_workspace_bytes(ctypes.byref(p), ctypes.byref(w), b) for b in (0, 1)]
+    for ws in (f[0], f[1], f[2], f[5], f[6], at(f[0], -need[0] + 16)):
+        assert L.ep_lora(ctypes.byref(p), ctypes.byref(lay), ctypes.byref(w), f[0], 0, f[1], 0, f[2], 0, ws, need[0],
+                         None) == _lib.EP_EINVAL, ws
+    gbase = ctypes.c_void_p(11 << 40)
+    for ws in (f[0], f[1], f[2], f[3], f[4], f[5], f[6], gbase, at(f[3], -need[1] + 16)):
+        assert L.ep_lora_backward(ctypes.byref(p), ctypes.byref(lay), ctypes.byref(w), f[0], 0, f[1], 0, gbase, 0, f[2], 0,
+                                  f[3], f[4], ws, need[1], None) == _lib.EP_EINVAL, ws
+
+
+def test_binding_keeps_int32_fields_whole():
+    for fields in ((4, 8, 2, 0, 0, 1 << 32, 0, 1, 0, 1.0), (4, 8, 2, 1 << 32, 0, 0, 0, 1, 0, 1.0),
+                   (4, (1 << 32) + 8, 2, 0, 0, 0, 0, 1, 0, 1.0)):
+        with pytest.raises(ValueError, match="int32"):
+            layer._router_struct(*fields)
+    lay = ep.Layout(4, 2, 3, 0, *(torch.zeros(4, dtype=torch.int32) for _ in range(4)))
+    for sizes in (((1 << 32) + 16, 16, 8), (16, (1 << 32) + 16, 8), (16, 16, (1 << 32) + 8)):
+        with pytest.raises(ValueError, match="int32"):
+            ep.ep_lora_workspace_bytes(lay, *sizes)
+
+
 def test_binding_refusals():
     z = torch.zeros
     with pytest.raises(ValueError, match="device tensor"):
