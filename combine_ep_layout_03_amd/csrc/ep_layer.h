@@ -83,6 +83,8 @@ struct LoraGeom {
   size_t expand_bytes, chunk_bytes, u_bytes, v_bytes, slot_bytes;
   size_t bytes() const { return expand_bytes + chunk_bytes + u_bytes + v_bytes + slot_bytes; }
 };
+// blocks that write the rows of no selection, at most
+constexpr int64_t kLoraMaxCopyBlocks = 2048;
 LoraGeom lora_geom(int64_t rows, int E, int H, int N, int R, bool backward);
 
 struct LoraArgs {
@@ -101,7 +103,7 @@ struct LoraArgs {
   const int32_t* offsets;
   const int32_t* slot;  // [T], to find the tokens of no row (omap only)
   int64_t T;
-  int E, H, N, R;
+  int K, E, H, N, R;
   // backward: grad_out [.., N] with omap's rows, base and out are [.., H]
   const uint16_t* go;
   int64_t ldgo;

@@ -116,9 +116,10 @@ int check_lora(const ep_problem_t* p, const ep_lora_weights_t* w) {
   // grid limits: fewer than 2^32 threads, and 2^31 row indices (check_problem)
   if (static_cast<int64_t>(p->hidden) + w->n_out > (1 << 24)) return EP_ENOTSUP;
   const ep::LoraGeom g = geom_of(p, w, true);
-  const int64_t cols = (p->hidden > w->n_out ? p->hidden : w->n_out) / 512 + 1 + 16;  // and the copies'
+  const int64_t cols = (p->hidden > w->n_out ? p->hidden : w->n_out) / 512 + 1;
   if (g.max_tiles >= (1 << 23) ||
-      g.max_expand * cols + ep::lora_weight_blocks(g, p->hidden, w->n_out, w->rank) >= (1 << 24))
+      g.max_expand * cols + ep::kLoraMaxCopyBlocks + ep::lora_weight_blocks(g, p->hidden, w->n_out, w->rank) >=
+          (1 << 24))
     return EP_ENOTSUP;
   return EP_OK;
 }
@@ -139,6 +140,7 @@ int lora_args(const ep_problem_t* p, const ep_layout_t* L, const ep_lora_weights
   a->offsets = L->offsets;
   a->slot = L->slot;
   a->T = p->num_tokens;
+  a->K = p->topk;
   a->E = p->num_experts;
   a->H = p->hidden;
   a->N = w->n_out;

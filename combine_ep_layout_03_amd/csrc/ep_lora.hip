@@ -28,13 +28,13 @@
 //
 // Measured (a plain copy: 4.98 TB/s):
 //     16,384 rows, 4096 -> 2048, rank 32, 64 experts, in expert order
-//       forward   shrink 39 us (x 134 MB), expand 37 us (base and out 134 MB)
-//       backward  shrink 66 us, gradients 72 us (x and g again, 201 MB; base and
-//                 dx, 268 MB), join 5 us
+//       forward   shrink 32 us (x 134 MB), expand 36 us (base and out 134 MB)
+//       backward  shrink 55 us (x and g 201 MB), gradients 68 us (x and g again,
+//                 and dx, 134 MB), join 5 us
 //     8111 tokens, 7168 -> 2048, rank 64, 10% without an adapter
-//       forward   shrink 31 us (x 105 MB), expand 26 us (base and out 66 MB)
-//     61 tokens, 4096 -> 4096, rank 16: 4.9 + 5.5 us; 509 tokens, rank 8, backward:
-//       7.2 + 8.4 + 3.6 us.  Launch, tile search and three dependent loads are
+//       forward   shrink 27 us (x 105 MB), expand 18 us (base and out 66 MB)
+//     61 tokens, 4096 -> 4096, rank 16: 5.1 + 5.5 us; 509 tokens, rank 8, backward:
+//       7.0 + 8.6 + 3.5 us.  Launch, tile search and three dependent loads are
 //       most of these.
 // The matrix units are busy for at most a tenth of a kernel's time: memory's
 // latency and rate bound the long ones.
@@ -49,7 +49,6 @@ namespace {
 constexpr int kCols = 128;  // columns of one wave
 constexpr int kXcds = 8;
 constexpr int kMaxSplits = 4;  // splits of a contraction over blocks
-constexpr int kMaxCopyColumns = 16;
 
 __device__ __forceinline__ f32x4_t mfma(u32x4 a, u32x4 b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
@@ -57,6 +56,11 @@ __device__ __forceinline__ f32x4_t mfma(u32x4 a, u32x4 b, f32x4_t c) {
 }
 
 __device__ __forceinline__ u32x4 load16(const uint16_t* p) { return *reinterpret_cast<const u32x4*>(p); }
+// STREAM: non-temporal, for the last read of rows that the caches could not keep.
+template <bool STREAM>
+__device__ __forceinline__ u32x4 load_row16(const uint16_t* p) {
+  return STREAM ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)) : load16(p);
+}
 
 // LDS that one wave alone uses is accessed in order: only the compiler has to
 // keep the order.
@@ -186,6 +190,7 @@ struct ShrinkArgs {
   float* part;     // [S, rows, R]
   int64_t stride;  // rows * R
   int S;
+  bool streamed;  // the rows are not read again and too many for the caches
   // tiles of the kernels to come, written by two waves of split 0's blocks
   int32_t* expand_tiles;  // num_expand == 0: none
   int num_expand, expand_shift;
@@ -220,7 +225,7 @@ struct ShrinkLds {
   static constexpr int kBytes = NW * kRed * 4 > kWBytes + kXBytes ? NW * kRed * 4 : kWBytes + kXBytes;
 };
 
-template <int RT, int MT, int NW, bool KMAJOR>
+template <int RT, int MT, int NW, bool KMAJOR, bool STREAM>
 __device__ __forceinline__ void shrink(const ShrinkArgs& a, char* s_mem) {
   using Lds = ShrinkLds<RT, MT, NW, KMAJOR>;
   constexpr int kShift = MT == 1 ? 4 : MT == 2 ? 5 : 6;
@@ -282,7 +287,7 @@ __device__ __forceinline__ void shrink(const ShrinkArgs& a, char* s_mem) {
   auto past = [&](int p) __attribute__((always_inline)) { return p * 64 + unit * 8 >= a.C; };
   auto load_x = [&](int p, u32x4 (&x)[2 * MT]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int n = 0; n < 2 * MT; ++n) x[n] = load16(xr[n] + place(p));
+    for (int n = 0; n < 2 * MT; ++n) x[n] = load_row16<STREAM>(xr[n] + place(p));
   };
   auto put_x = [&](int p, u32x4 (&x)[2 * MT]) __attribute__((always_inline)) {
 #pragma unroll
@@ -394,7 +399,8 @@ __device__ __forceinline__ void shrink(const ShrinkArgs& a, char* s_mem) {
 template <int RT, int MT, int NW>
 __global__ __launch_bounds__(NW* kWave) void k_lora_shrink(ShrinkArgs a) {
   __shared__ __align__(16) char s_mem[ShrinkLds<RT, MT, NW, false>::kBytes];
-  shrink<RT, MT, NW, false>(a, s_mem);
+  if (a.streamed) shrink<RT, MT, NW, false, true>(a, s_mem);
+  else shrink<RT, MT, NW, false, false>(a, s_mem);
 }
 
 // u and v of the backward pass in one launch: 509 rows x 4096, rank 8: 7.1 us
@@ -404,8 +410,8 @@ template <int RT, int MT, int NW>
 __global__ __launch_bounds__(NW* kWave) void k_lora_shrink_both(ShrinkArgs u, ShrinkArgs v) {
   constexpr int kU = ShrinkLds<RT, MT, NW, false>::kBytes, kV = ShrinkLds<RT, MT, NW, true>::kBytes;
   __shared__ __align__(16) char s_mem[kU > kV ? kU : kV];
-  if (blockIdx.z == 0) shrink<RT, MT, NW, false>(u, s_mem);
-  else shrink<RT, MT, NW, true>(v, s_mem);
+  if (blockIdx.z == 0) shrink<RT, MT, NW, false, false>(u, s_mem);
+  else shrink<RT, MT, NW, true, false>(v, s_mem);
 }
 
 // ------------------------------------------------------------------- expand
@@ -535,7 +541,6 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, int64_t index, int c
   int* const s_row = reinterpret_cast<int*>(s_mem + (PACK ? 1 : 2) * Lds::kU * 2);
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
-  if (index >= a.num_tiles) return;
   const Tile t = stored_tile(a.tiles, static_cast<int>(index));
   if (t.e < 0) return;
   const int n0 = (col_block * 4 + wave) * kCols;
@@ -640,7 +645,7 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, int64_t index, int c
         if (with_base.value) load_base(next, base[d]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          *reinterpret_cast<u32x4*>(a.out + row[d][i] * a.ldout + n) = o[i];
+          __builtin_nontemporal_store(o[i], reinterpret_cast<u32x4*>(a.out + row[d][i] * a.ldout + n));
           row[d][i] = next[i];
         }
       }
@@ -666,20 +671,27 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, int64_t index, int c
   }
 }
 
+// Block `block` of `blocks`: the columns of a tile fastest, and after the tiles
+// the rows of no selection.  (As further columns of the tiles the copies were on
+// the same XCDs throughout wherever all columns together were a multiple of 8.)
+template <int KS, bool PACK, bool JMAJOR>
+__device__ __forceinline__ void expand_block(const ExpandArgs& a, unsigned block, unsigned blocks, char* s_mem) {
+  const unsigned ncb = static_cast<unsigned>((a.N + 4 * kCols - 1) / (4 * kCols));
+  const unsigned tiles = static_cast<unsigned>(a.num_tiles) * ncb;
+  if (block < tiles) {
+    expand<KS, PACK, JMAJOR>(a, block / ncb, static_cast<int>(block % ncb), s_mem);
+  } else {
+    copy_unselected(a, static_cast<int64_t>(block - tiles) * kCopyTokens,
+                    static_cast<int64_t>(blocks - tiles) * kCopyTokens);
+  }
+}
+
 template <int KS, bool PACK>
 __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(KS == 1 ? 3 : 2))) void k_lora_expand(
     ExpandArgs a) {
   __shared__ __align__(16) char s_mem[ExpandLds<KS, PACK>::kBytes];
   if (!layout_current(a.status, a.generation)) return;
-  const int64_t index = static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y;
-  const int ncb = (a.N + 4 * kCols - 1) / (4 * kCols);
-  if (static_cast<int>(blockIdx.x) >= ncb) {  // the columns of rows of no selection
-    const int64_t copies = gridDim.x - ncb;
-    copy_unselected(a, (index * copies + blockIdx.x - ncb) * kCopyTokens,
-                    copies * gridDim.y * gridDim.z * kCopyTokens);
-    return;
-  }
-  expand<KS, PACK, false>(a, index, static_cast<int>(blockIdx.x), s_mem);
+  expand_block<KS, PACK, false>(a, blockIdx.x, gridDim.x, s_mem);
 }
 
 // --------------------------------------------------------- weight gradients
@@ -697,6 +709,7 @@ struct WeightGradArgs {
   int64_t slot_size;  // R * (H + N)
   const float* scales;
   int R, E, shift;
+  bool streamed;
   const int32_t* chunks;
   const int32_t* counts;
   int32_t* status;
@@ -710,7 +723,7 @@ __host__ __device__ constexpr int staged_rows(int JT) { return 256 / JT; }
 // R.  A wave takes 32 rows by 128 columns per step, one or two steps in flight, loaded
 // without a condition (see k_lora_expand).  A lane ends with R's 4 q + i (i < 4)
 // of each 16 and 8 neighbouring columns.
-template <int JT, int NW, int B>
+template <int JT, int NW, int B, bool STREAM>
 __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile& t, int cb, int jg, uint16_t* s_hi,
                                             uint16_t* s_lo, int* s_row) {
   constexpr int kStaged = staged_rows(JT);
@@ -735,7 +748,7 @@ __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile&
   const uint16_t* in = a.in[B] + min(col, C - 8);
   auto load_step = [&](int r, u32x4 (&v)[8]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = load16(in + s_row[min(r + q * 8 + i, t.nrows - 1)] * a.ld[B]);
+    for (int i = 0; i < 8; ++i) v[i] = load_row16<STREAM>(in + s_row[min(r + q * 8 + i, t.nrows - 1)] * a.ld[B]);
   };
   constexpr int kAhead = JT <= 2 ? 2 : 1;  // steps in flight, as registers allow
   u32x4 v[kAhead][8];
@@ -839,7 +852,7 @@ __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile&
 // blocks take the weight gradients, the longer work, the others tiles of dx.
 template <int KS, bool PACK, int JT>
 __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(2))) void k_lora_gradients(
-    WeightGradArgs w, ExpandArgs x, unsigned weight_blocks, int copy) {
+    WeightGradArgs w, ExpandArgs x, unsigned weight_blocks) {
   constexpr int kElems = JT * 16 * (staged_rows(JT) + 8);
   constexpr int kW = 4 * kElems, kX = ExpandLds<KS, PACK>::kBytes;
   __shared__ __align__(16) char s_mem[kW > kX ? kW : kX];
@@ -858,16 +871,15 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(2))) voi
     const Tile t = stored_tile(w.chunks, at / jgs);
     if (t.e < 0) return;
     uint16_t* const s_hi = reinterpret_cast<uint16_t*>(s_mem);
-    if (cb < nca) weight_grad<JT, kWavesPerBlock, 0>(w, t, cb, jg, s_hi, s_hi + kElems, s_row);
-    else weight_grad<JT, kWavesPerBlock, 1>(w, t, cb - nca, jg, s_hi, s_hi + kElems, s_row);
+    auto grad = [&](auto stream) __attribute__((always_inline)) {
+      constexpr bool kStream = decltype(stream)::value;
+      if (cb < nca) weight_grad<JT, kWavesPerBlock, 0, kStream>(w, t, cb, jg, s_hi, s_hi + kElems, s_row);
+      else weight_grad<JT, kWavesPerBlock, 1, kStream>(w, t, cb - nca, jg, s_hi, s_hi + kElems, s_row);
+    };
+    if (w.streamed) grad(std::integral_constant<bool, true>());
+    else grad(std::integral_constant<bool, false>());
   } else {
-    const int ncb = (x.N + 4 * kCols - 1) / (4 * kCols);
-    const int cols = ncb + copy;
-    const int at = static_cast<int>(blockIdx.x - weight_blocks);
-    const int cb = at % cols;
-    if (cb >= ncb) copy_unselected(x, (static_cast<int64_t>(at / cols) * copy + cb - ncb) * kCopyTokens,
-                                   x.num_tiles * copy * kCopyTokens);
-    else expand<KS, PACK, true>(x, at / cols, cb, s_mem);
+    expand_block<KS, PACK, true>(x, blockIdx.x - weight_blocks, gridDim.x - weight_blocks, s_mem);
   }
 }
 
@@ -952,20 +964,19 @@ hipError_t launch_shrink(const ShrinkArgs& u, const ShrinkArgs* v, const LoraGeo
   return hipGetLastError();
 }
 
-// Columns of blocks that write the rows of no selection, beside the result's:
-// 0 where there are none to write.
-int64_t copy_columns(const ExpandArgs& a) {
-  if (!a.map || a.base == a.out) return 0;
-  const int64_t blocks = (a.T + kCopyTokens - 1) / kCopyTokens;
-  const int64_t n = (blocks + a.num_tiles - 1) / a.num_tiles;
-  return n < kMaxCopyColumns ? n : kMaxCopyColumns;
+// Blocks of a result: its tiles', and those that write the rows of no selection
+// where there may be any to write.
+unsigned expand_blocks(const ExpandArgs& a) {
+  int64_t n = a.num_tiles * ((a.N + 4 * kCols - 1) / (4 * kCols));
+  if (a.map && a.base != a.out) {
+    const int64_t copies = (a.T + kCopyTokens - 1) / kCopyTokens;
+    n += copies < kLoraMaxCopyBlocks ? copies : kLoraMaxCopyBlocks;
+  }
+  return static_cast<unsigned>(n);
 }
 
 hipError_t launch_expand(const ExpandArgs& a, hipStream_t s) {
-  const unsigned ncb = static_cast<unsigned>((a.N + 4 * kCols - 1) / (4 * kCols));
-  const unsigned ny = static_cast<unsigned>(a.num_tiles < 65528 ? a.num_tiles : 65528);  // dimension limit
-  const unsigned nz = static_cast<unsigned>((a.num_tiles + ny - 1) / ny);
-  const dim3 grid(ncb + static_cast<unsigned>(copy_columns(a)), ny, nz);
+  const unsigned grid = expand_blocks(a);
   if (a.R <= 16) k_lora_expand<1, true><<<grid, kBlock, 0, s>>>(a);
   else if (a.R <= 32) k_lora_expand<1, false><<<grid, kBlock, 0, s>>>(a);
   else if (a.R <= 64) k_lora_expand<2, false><<<grid, kBlock, 0, s>>>(a);
@@ -975,13 +986,12 @@ hipError_t launch_expand(const ExpandArgs& a, hipStream_t s) {
 
 hipError_t launch_gradients(const WeightGradArgs& w, const ExpandArgs& x, const LoraGeom& g, hipStream_t s) {
   const unsigned wb = static_cast<unsigned>(lora_weight_blocks(g, w.C[0], w.C[1], w.R));
-  const int copy = static_cast<int>(copy_columns(x));
-  const unsigned blocks = wb + static_cast<unsigned>(x.num_tiles * ((x.N + 4 * kCols - 1) / (4 * kCols) + copy));
+  const unsigned blocks = wb + expand_blocks(x);
   const size_t lds = sizeof(int) << g.chunk_shift;
-  if (w.R <= 16) k_lora_gradients<1, true, 1><<<blocks, kBlock, lds, s>>>(w, x, wb, copy);
-  else if (w.R <= 32) k_lora_gradients<1, false, 2><<<blocks, kBlock, lds, s>>>(w, x, wb, copy);
-  else if (w.R <= 64) k_lora_gradients<2, false, 4><<<blocks, kBlock, lds, s>>>(w, x, wb, copy);
-  else k_lora_gradients<4, false, 4><<<blocks, kBlock, lds, s>>>(w, x, wb, copy);
+  if (w.R <= 16) k_lora_gradients<1, true, 1><<<blocks, kBlock, lds, s>>>(w, x, wb);
+  else if (w.R <= 32) k_lora_gradients<1, false, 2><<<blocks, kBlock, lds, s>>>(w, x, wb);
+  else if (w.R <= 64) k_lora_gradients<2, false, 4><<<blocks, kBlock, lds, s>>>(w, x, wb);
+  else k_lora_gradients<4, false, 4><<<blocks, kBlock, lds, s>>>(w, x, wb);
   return hipGetLastError();
 }
 
@@ -1000,6 +1010,18 @@ ShrinkArgs shrink_args(const LoraArgs& a, const LoraGeom& g) {
   s.status = a.status;
   s.generation = a.generation;
   return s;
+}
+
+// Are the rows of this many columns too large to be found in the caches (256 MB
+// beside the memory, shared with all else) by whoever reads them next?  Read for
+// the last time here, they then make room for what is: the shrink of 8111 x 7168
+// takes 27 us against 32, of 8192 x 4096 (64 MB) 19 against 21, while a caller's
+// second use of 2048 x 7168 (29 MB) would cost 18 against 14; the weight
+// gradients of 16,384 x 4096 + 2048 and the shrink before the next call's 122 us
+// against 127, of 2048 x 4096 + 4096 27.5 against 25.
+bool streamed(const LoraArgs& a, int64_t columns) {
+  const int64_t rows = a.T * a.K;
+  return rows * columns * 2 >= (64 << 20);
 }
 
 ExpandArgs expand_args(const LoraArgs& a, const LoraGeom& g) {
@@ -1038,22 +1060,26 @@ LoraGeom lora_geom(int64_t rows, int E, int H, int N, int R, bool backward) {
   else if (rows < 4096 && tiles > 2) tiles = 2;
   g.row_tiles = static_cast<int>(tiles < wide ? tiles : wide);
   g.max_tiles = up8(rows / (16 * g.row_tiles) + used);
-  // The contraction is split over blocks too until there are two per CU, as far
-  // as a split keeps 512 elements (61 rows x 4096: 4.9 us against 7.2 without;
-  // 8111 x 7168: 31 against 43; 16,384 x 4096: 39 against 44).
+  // The contraction is split over blocks too, as far as a split keeps 512
+  // elements, until there are four blocks per CU (61 rows x 4096: 4.9 us against
+  // 7.2 without; 8111 x 7168: 32 against 43; 16,384 x 4096: 36 against 41 with two
+  // per CU and 44 without), in the backward pass two (the weight gradients read
+  // every split's part again: 16,384 x 4096, both kernels, 133 us against 140 with
+  // four per CU and 135 with one).
+  const int enough = backward ? 512 : 1024;
   auto splits = [&](int C) {
     int n = 1;
-    while (n < kMaxSplits && g.max_tiles * n < 512 && C >= 512 * n) n *= 2;
+    while (n < kMaxSplits && g.max_tiles * n < enough && C >= 512 * n) n *= 2;
     return n;
   };
-  // The result's tiles: the longest that leave about two blocks per CU
-  // (16,384 rows x 4096: 28.0 us with 128 rows, 29.0 with 64, 35.6 with 32;
-  // 8111 x 2048 at rank 64: 35.7 us with 64, 36.6 with 128)
+  // The result's tiles: the longest of which the rows alone, in one expert, fill
+  // three quarters of the CUs (rank 64, 8111 x 2048: 20.9 us with 128 rows, 22.9
+  // with 64, 26.9 with 32; 2048 x 2048: 8.5 with 32, 10.9 with 16; rank 16, 1024 x
+  // 4096: 8.0 with 32, 8.8 with 16)
   const int64_t col_blocks = ((backward ? H : N) + 4 * kCols - 1) / (4 * kCols);
-  auto expand_tiles = [&](int shift) { return up8((rows >> shift) + used); };
   g.expand_shift = R <= 64 ? 7 : 6;
-  while (g.expand_shift > 4 && expand_tiles(g.expand_shift) * col_blocks < 500) --g.expand_shift;
-  g.max_expand = expand_tiles(g.expand_shift);
+  while (g.expand_shift > 4 && (rows >> g.expand_shift) * col_blocks < 192) --g.expand_shift;
+  g.max_expand = up8((rows >> g.expand_shift) + used);
   g.expand_bytes = static_cast<size_t>(g.max_expand) * 16;
   g.split_x = splits(H);
   g.u_bytes = static_cast<size_t>(up16(g.split_x * rows * R * 4));
@@ -1091,6 +1117,7 @@ hipError_t launch_lora(const LoraArgs& a, const LoraGeom& g, hipStream_t s) {
   u.C = a.H;
   u.part = a.u;
   u.S = g.split_x;
+  u.streamed = streamed(a, a.H);
   const hipError_t err = launch_shrink(u, nullptr, g, s);
   if (err != hipSuccess) return err;
   ExpandArgs x = expand_args(a, g);
@@ -1124,6 +1151,7 @@ hipError_t launch_lora_backward(const LoraArgs& a, const LoraGeom& g, hipStream_
   w.R = a.R;
   w.E = a.E;
   w.shift = g.chunk_shift;
+  w.streamed = streamed(a, a.H + a.N);
   w.chunks = a.chunks;
   w.counts = a.counts;
   w.status = a.status;
