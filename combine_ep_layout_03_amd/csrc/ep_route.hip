@@ -22,9 +22,9 @@
 // A wave does one task and ends: in a loop over tasks the compiler keeps what
 // does not change between them, some 400 instructions' results, and spills.
 //
-// Measured, 256 experts, top-8.  65,536 tokens, bf16 softmax: 19.5 us, 2 TB/s;
+// Measured, 256 experts, top-8.  65,536 tokens, bf16 softmax: 20 us, 2 TB/s;
 // the vector units issue for 16 of them (600 instructions a wave).  Sigmoid +
-// bias, 4 of 8 groups: 8192 tokens 12.8 us, two waves per SIMD, of which the
+// bias, 4 of 8 groups: 8192 tokens 13.0 us, two waves per SIMD, of which the
 // vector units issue for 5: the chain of dependent steps bounds it; 16 tokens 6.8
 // us, that chain once.  The binary64 path, every token's experts all equal:
 // 65,536 tokens 380 us (fp32 softmax) and 740 us (scored); in fp32 logits
