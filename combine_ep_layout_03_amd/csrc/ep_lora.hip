@@ -234,6 +234,7 @@ __device__ __forceinline__ void shrink(const ShrinkArgs& a, char* s_mem) {
   if (static_cast<int>(blockIdx.y) >= a.S) return;
   const int block = static_cast<int>(blockIdx.x);
   const Tile t = find_tile<true>(a.counts, a.offsets, a.E, kShift, block);
+  static_assert(NW > 2, "waves 1 and 2 write the tables");
   if (blockIdx.y == 0) {
     const int w = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
     auto table = [&](int32_t* out, int n, int shift) {
@@ -1051,10 +1052,12 @@ LoraGeom lora_geom(int64_t rows, int E, int H, int N, int R, bool backward) {
   const int64_t used = rows < E ? rows : E;  // experts with rows, at most
   const int64_t avg = rows / E;
   auto up8 = [](int64_t n) { return (n + kXcds - 1) / kXcds * kXcds; };
-  // Tiles of 64 rows read an expert's matrix least often (8111 rows x 7168, rank
-  // 64: 31 us against 46 with tiles of 16); smaller ones where its rows, or all
-  // rows, are few.
-  const int64_t wide = R <= 64 ? 4 : 2;  // registers
+  // Tiles of 64 rows read an expert's matrix less often (8111 rows x 7168, rank
+  // 64: 31 us against 46 with tiles of 16; tiles of 128 gain nothing more, 16,384
+  // x 4096 takes 34 us against 32); smaller ones where its rows, or all rows, are
+  // few, and above rank 64 for want of registers (rank 128: 16,384 x 4096 66 us
+  // with 32 rows, 72 with 64).
+  const int64_t wide = R <= 64 ? 4 : 2;
   int64_t tiles = avg >= 64 ? 4 : avg >= 32 ? 2 : 1;
   if (rows < 2048) tiles = 1;
   else if (rows < 4096 && tiles > 2) tiles = 2;
