@@ -182,6 +182,18 @@ def test_lora_backward(T, K, E, H, N, R, gather, scatter, A, pad):
     c.backward(base=True)
 
 
+@pytest.mark.parametrize("T,K,E,H,N,R,scatter", [(33_000, 1, 7, 1024, 264, 16, True), (17_000, 2, 70, 1000, 520, 40, False),
+                                                 (33_000, 1, 3, 1016, 72, 72, True)])
+def test_lora_more_rows_than_caches_keep(T, K, E, H, N, R, scatter):
+    """64 MiB of rows and more, loaded another way; more tokens without an
+    adapter than the blocks that copy them take at once."""
+    assert T * K * H * 2 >= 64 << 20 or T * K * (H + N) * 2 >= 64 << 20
+    c = Case(_ids(T, K, E, T + R, none=0.4), E, H, N, R, True, scatter, seed=R)
+    c.forward()
+    c.forward(inplace=True)
+    c.backward(base=True)
+
+
 @pytest.mark.parametrize("gather,scatter,K,T", [(True, True, 1, 150), (False, False, 2, 150), (True, True, 1, 2500),
                                                 (True, False, 2, 2500)])
 @pytest.mark.parametrize("R", [8, 16, 32, 72, 128])
