@@ -17,7 +17,8 @@
 // bias in binary64.  That takes one binary64 score per candidate, for the
 // candidates down to the first clear gap below the Kth.  Groups are treated
 // alike.  Where even that leaves doubt (too many candidates, a group whose best
-// two are in doubt) the token is done again in binary64 throughout.
+// two are in doubt) the token is done again, by fp32 logits in rounds on the
+// logits themselves, else in binary64 throughout.
 //
 // A wave does one task and ends: in a loop over tasks the compiler keeps what
 // does not change between them, some 400 instructions' results, and spills.
@@ -26,9 +27,10 @@
 // the vector units issue for 16 of them (600 instructions a wave).  Sigmoid +
 // bias, 4 of 8 groups: 8192 tokens 13.0 us, two waves per SIMD, of which the
 // vector units issue for 5: the chain of dependent steps bounds it; 16 tokens 6.8
-// us, that chain once.  The binary64 path, every token's experts all equal:
-// 65,536 tokens 380 us (fp32 softmax) and 740 us (scored); in fp32 logits
-// that hold bf16 values, with their many ties, 37 us against 33 without ties.
+// us, that chain once.  fp32 softmax: 65,536 tokens 28 us, 33 where the logits
+// hold bf16 values with their many ties, 66 where a token's are all equal (380
+// before those had rounds of their own); the binary64 path, all scores equal:
+// 740.
 #include <float.h>
 
 #include "ep_layer.h"
@@ -598,6 +600,7 @@ __global__ __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) void
           all_keys[i] = (open >> group_of(expert(i), magic)) & 1 ? all_keys[i] : 0u;
       }
     }
+    const bool group_doubt = doubt;
     uint32_t key[KEEP];
     keep_largest(all_keys, key);
     auto close = [&](uint32_t x, uint32_t y) {
@@ -622,13 +625,15 @@ __global__ __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) void
         for (int i = 0; i < kOut; ++i) chosen[i] = k == g + i * LPT ? e : chosen[i];
       }
     } else {
+      // candidates worth keeping: exact rounds by logits cost little more
+      const int limit = BY == kByFp32 ? K + 4 : kCand;
       int taken = 0;  // of this lane's keys
       uint32_t prev = 0;
       for (int k = 0;; ++k) {
         const uint32_t m = over_token<LPT>(key[0], Max());
         if (k >= K) {  // beyond the Kth, down to the first clear gap
           if (prev == 0u || m == 0u || !close(prev, m)) break;
-          if (count == kCand) {
+          if (count == limit) {
             doubt = true;
             break;
           }
@@ -673,7 +678,31 @@ __global__ __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) void
         lds_sync();
       }
     }
-    if (doubt) {
+    if (BY == kByFp32 && doubt && !group_doubt) {
+      // a round after the other by the logits themselves (a row of equal ones)
+      float v[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        v[i] = kNegInf;
+        if (expert(i) < E && ((open >> (a.G ? group_of(expert(i), magic) : 0)) & 1))
+          v[i] = clean_logit(raw_logit(row + expert(i)));
+      }
+      for (int k = 0; k < K; ++k) {
+        float best = kNegInf;
+        uint32_t at = UINT32_MAX;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          at = v[i] > best ? static_cast<uint32_t>(expert(i)) : at;
+          best = fmaxf(best, v[i]);
+        }
+        const float most = over_token<LPT>(best, Max());
+        const uint32_t win = over_token<LPT>(best == most ? at : UINT32_MAX, Min());
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = static_cast<uint32_t>(expert(i)) == win ? kNegInf : v[i];
+#pragma unroll
+        for (int i = 0; i < kOut; ++i) chosen[i] = k == g + i * LPT ? static_cast<int>(win) : chosen[i];
+      }
+    } else if (doubt) {
       // one token after the other: its values take the whole array
       for (int d = 0; d < kTok; ++d)
         if (d == tok) choose64<LPT>(a, row, g, lmax, reinterpret_cast<double*>(s_val), gv, idxs);

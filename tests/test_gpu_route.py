@@ -198,6 +198,34 @@ def test_route_all_experts_equal():
             _check(l, 8, "sigmoid", bias=torch.zeros(E), G=4, TG=2, gtop=2, renorm=True, copies=copies)
 
 
+@pytest.mark.parametrize("E", [64, 256, 512, 1000])
+@pytest.mark.parametrize("K", [1, 8, 17, 32])
+def test_route_ties_and_experts_of_one_lane(E, K):
+    """fp32 logits with more equal ones than are kept as candidates, across the
+    Kth place and above it, with NaN and -inf between them, and with the
+    largest ones all held by one lane."""
+    g = torch.Generator().manual_seed(E + K)
+    l = torch.randn(10, E, generator=g)
+    l[0] = 0.25
+    l[1, ::3], l[1, 1::3] = float("nan"), 1.0
+    l[2, : E // 2] = float("-inf")
+    l[2, E // 2:] = -2.5
+    l[3] = torch.where(torch.rand(E, generator=g) < 0.5, 3.0, l[3])
+    l[4, torch.randperm(E, generator=g)[: K - 1]] = 9.0
+    l[4, torch.randperm(E, generator=g)[: E // 2]] = 4.0
+    for i, lanes in enumerate((16, 32, 64)):  # lane 3's experts of 16, 32 or 64 lanes a token
+        held = [e for e in range(E) if e // 4 % lanes == 3]
+        l[5 + i, held] += 10.0
+    l[8] = l[8].to(torch.bfloat16).float()
+    l[9, 1:] = float("nan")
+    for copies in (1, 230):
+        _check(l, K, copies=copies)
+        _check(l, K, "sigmoid", renorm=True, copies=copies)
+        if E % 8 == 0 and K <= E // 4:
+            _check(l, K, G=8, TG=3, copies=copies)
+            _check(l, K, G=8, TG=3, gtop=2, copies=copies)
+
+
 def test_route_offsets_past_32_bits():
     """9 million tokens x 256 bf16 logits, 4.6 GB: the last tokens as in a call
     of their own, and the gradient likewise."""
