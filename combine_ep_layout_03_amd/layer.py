@@ -40,19 +40,34 @@ def _check(t: torch.Tensor, name: str, dtype: torch.dtype, shape, index: int) ->
 
 
 def _rows(t: torch.Tensor, name: str, width: int, rows: int, index: int) -> torch.Tensor:
+    if (
+        isinstance(t, torch.Tensor)
+        and t.dtype is _BF16
+        and t.is_cuda
+        and t.is_contiguous()
+        and t.get_device() == index
+    ):
+        have = t.shape
+        if len(have) == 2 and have[1] >= width and have[0] >= rows:
+            return t
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be [rows, >= {width}]")
     _check(t, name, _BF16, None, index)
-    have = t.shape
-    if have[1] < width or have[0] < rows:
-        raise ValueError(f"{name} must be at least [{rows}, {width}], got {tuple(have)}")
-    return t
+    raise ValueError(f"{name} must be at least [{rows}, {width}], got {tuple(t.shape)}")
+
+
+def _row_like(t: torch.Tensor | None, rows: int, width: int, other: torch.Tensor) -> torch.Tensor:
+    """A new [rows, width] of bf16 on `other`'s GPU; made after `t` where that
+    has the shape, which is quicker."""
+    if t is not None and t.shape == (rows, width):
+        return torch.empty_like(t)
+    return other.new_empty((rows, width))
 
 
 def _call(fn: str, index: int, *args) -> None:
     """The library's `fn` on GPU `index` and its current stream: the library
     launches on the current device."""
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         rc = getattr(_lib.lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
@@ -151,8 +166,8 @@ def ep_route(
             raise TypeError("token_mask must be bool or uint8")
         _check(token_mask, "token_mask", token_mask.dtype, (T,), index)
     if out is None:
-        idx = torch.empty((T, K), dtype=_I64, device=logits.device)
-        w = torch.empty((T, K), dtype=_F32, device=logits.device)
+        idx = logits.new_empty((T, K), dtype=_I64)
+        w = logits.new_empty((T, K), dtype=_F32)
     else:
         idx, w = out
         _check(idx, "out[0]", _I64, (T, K), index)
@@ -218,7 +233,7 @@ def ep_combine_backward(
     else:
         _check(grad_y, "grad_y", _BF16, (rows, H), index)
     if grad_weights is None:
-        grad_weights = torch.empty((T, K), dtype=_F32, device=y.device)
+        grad_weights = torch.empty_like(topk_weights)
     else:
         _check(grad_weights, "grad_weights", _F32, (T, K), index)
     _layout_index(layout, index)
@@ -270,8 +285,7 @@ def _lora_args(layout, gen, a, b, scales, gather, scatter, backward, workspace):
     shape = (T, H, layout.topk, E, layout.num_groups, layout.expert_alignment,
              _lib.EP_FLAG_GATHER_ROWS if gather else 0)
     if workspace is None:
-        need = _lora_workspace(*shape, R, N, wflags, backward)
-        workspace = torch.empty(need, dtype=_U8, device=a.device)
+        workspace = a.new_empty(_lora_workspace(*shape, R, N, wflags, backward), dtype=_U8)
     else:
         _check(workspace, "workspace", _U8, None, index)
     w = _lib.LoraWeights(a.data_ptr(), b.data_ptr(), _ptr(scales), R, N, wflags)
@@ -312,7 +326,7 @@ def ep_lora(
     if base is not None:
         _rows(base, "base", N, orows, index)
     if out is None:
-        out = torch.empty((orows, N), dtype=_BF16, device=x.device)
+        out = _row_like(base, orows, N, x)
     else:
         _rows(out, "out", N, orows, index)
     _call("ep_lora", index, p, s, w, x.data_ptr(), x.shape[1], _ptr(base), 0 if base is None else base.shape[1],
@@ -354,7 +368,7 @@ def ep_lora_backward(
     if grad_base is not None:
         _rows(grad_base, "grad_base", H, orows, index)
     if grad_x is None:
-        grad_x = torch.empty((orows, H), dtype=_BF16, device=x.device)
+        grad_x = _row_like(x, orows, H, x)
     else:
         _rows(grad_x, "grad_x", H, orows, index)
     if grad_a is None:
