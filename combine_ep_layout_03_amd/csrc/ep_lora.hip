@@ -12,9 +12,12 @@
 //   expand   out or dx: a tile of rows by 128 columns per wave, contraction R
 //   weights  dA and dB: 128 columns per wave against all of R, contraction
 //            over a chunk of an expert's rows
-// u and v enter the second product as two bf16 parts, high and low: 16
-// significand bits, so the result is as good as its own bf16 rounding allows
-// (one bf16 part alone would add an error of the size of that rounding).
+// u and v enter the second product as three bf16 parts of 8 significand bits
+// each, which together are the fp32 value: nothing is rounded between the two
+// products.  (With two parts, 16 bits, up to 0.2% of the results were rounded
+// the other way; the third costs 72 us instead of 69 in the weight gradients of
+// 16,384 rows x 4096 -> 2048, rank 32, 179 instead of 162 at rank 128, and
+// nothing that shows elsewhere.)
 //
 // A matrix whose contraction index is not contiguous in memory is transposed
 // in registers: a lane loads 8 rows of 8 columns and forms, with 32 byte
@@ -69,11 +72,22 @@ __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// f as bf16 parts hi + lo.  Where hi is infinite lo is 0, not inf - inf.
-__device__ __forceinline__ void split(float f, uint16_t& hi, uint16_t& lo) {
-  hi = bf16_of(f);
-  const float h = bf16_to_f32(hi);
-  lo = fabsf(h) < __builtin_inff() ? bf16_of(f - h) : 0;
+// f as the sum of three bf16 parts, each the leading 8 significand bits of what
+// the ones before leave: exact, but for bits below bf16's smallest denormal,
+// 2^-133.  The parts have f's sign or are zero, so no sum of them overflows
+// that f does not, and the largest fp32 stays finite.  Every part of an
+// infinity or NaN is that infinity or a NaN.
+constexpr int kParts = 3;
+__device__ __forceinline__ void split(float f, uint16_t (&part)[kParts]) {
+  const uint32_t b = __float_as_uint(f);
+  const float r = f - __uint_as_float(b & 0xffff0000u);
+  const uint32_t c = __float_as_uint(r);
+  const float last = r - __uint_as_float(c & 0xffff0000u);
+  const bool finite = (b & 0x7f800000u) != 0x7f800000u;
+  // what a NaN's upper half has lost must not make it an infinity
+  part[0] = static_cast<uint16_t>(f == f ? b >> 16 : 0x7fc0u);
+  part[1] = finite ? static_cast<uint16_t>(c >> 16) : part[0];
+  part[2] = finite ? static_cast<uint16_t>(__float_as_uint(last) >> 16) : part[0];
 }
 
 // Column m of the 8 x 8 block held as rows v[0..7] of 8 columns.
@@ -503,43 +517,39 @@ __device__ __forceinline__ void joined_quads(int S, int count, int64_t stride, A
   else if (S == 2) joined_quads<2>(count, stride, at, put);
   else joined_quads<4>(count, stride, at, put);
 }
-__device__ __forceinline__ void split4(f32x4_t f, u32x2& hi, u32x2& lo) {
-  uint16_t h[4], l[4];
+__device__ __forceinline__ void split4(f32x4_t f, u32x2 (&part)[kParts]) {
+  uint16_t h[4][kParts];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) split(f[i], h[i], l[i]);
+  for (int i = 0; i < 4; ++i) split(f[i], h[i]);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    hi[i] = h[2 * i] | (static_cast<uint32_t>(h[2 * i + 1]) << 16);
-    lo[i] = l[2 * i] | (static_cast<uint32_t>(l[2 * i + 1]) << 16);
-  }
+  for (int d = 0; d < kParts; ++d)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) part[d][i] = h[2 * i][d] | (static_cast<uint32_t>(h[2 * i + 1][d]) << 16);
 }
 
 // Rows of a result tile at most, as much of u as LDS holds comfortably.
 __host__ __device__ constexpr int expand_rows(int KS) { return KS <= 2 ? 128 : 64; }
 
 // Block: one tile of rows by 512 columns.  u's rows are put into LDS, as their
-// two bf16 parts; a wave holds its 128 columns of the matrix in registers and
+// bf16 parts; a wave holds its 128 columns of the matrix in registers and
 // takes the tile's rows 16 at a time, the next 32 rows' base in flight.  The
 // loop over whole groups has no condition inside: memory operations complete in
 // order, and with a load or store that may be skipped the compiler waits for
-// all of them instead of counting.  PACK: R <= 16, the high parts in the first
-// half of one contraction step and the low parts in the second (8111 x 2048,
-// rank 16: 18.6 us against 19.9 with two products).
-template <int KS, bool PACK>
+// all of them instead of counting.
+template <int KS>
 struct ExpandLds {
   static constexpr int kPitch = KS * 32 + 8;
   static constexpr int kStaged = expand_rows(KS);
-  static constexpr int kU = kStaged * kPitch;  // elements of one part
-  static constexpr int kBytes = (PACK ? 1 : 2) * kU * 2 + kStaged * 4;
+  static constexpr int kPart = kStaged * kPitch;  // elements of one part
+  static constexpr int kBytes = kParts * kPart * 2 + kStaged * 4;
 };
 
-template <int KS, bool PACK, bool JMAJOR>
+template <int KS, bool JMAJOR>
 __device__ __forceinline__ void expand(const ExpandArgs& a, int64_t index, int col_block, char* s_mem) {
-  using Lds = ExpandLds<KS, PACK>;
+  using Lds = ExpandLds<KS>;
   constexpr int kPitch = Lds::kPitch, kStaged = Lds::kStaged;
-  uint16_t* const s_hi = reinterpret_cast<uint16_t*>(s_mem);
-  uint16_t* const s_lo = s_hi + (PACK ? 16 : Lds::kU);  // PACK: behind the high parts of each row
-  int* const s_row = reinterpret_cast<int*>(s_mem + (PACK ? 1 : 2) * Lds::kU * 2);
+  uint16_t* const s_u = reinterpret_cast<uint16_t*>(s_mem);
+  int* const s_row = reinterpret_cast<int*>(s_mem + kParts * Lds::kPart * 2);
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const Tile t = stored_tile(a.tiles, static_cast<int>(index));
@@ -562,7 +572,7 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, int64_t index, int c
   u32x4 wv[KS][8];
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) {
-    const int j = PACK ? (q & 1) * 8 : ks * 32 + q * 8;
+    const int j = ks * 32 + q * 8;
     u32x4 v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -577,7 +587,7 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, int64_t index, int c
       for (int i = 0; i < 8; ++i) wv[ks][i] = v[i];
     }
   }
-  constexpr int kQuads = PACK ? 4 : KS * 8;  // of a row, the ones past R zeros
+  constexpr int kQuads = KS * 8;  // of a row, the ones past R zeros
   const int groups = (t.nrows + 15) / 16;
   joined_quads(
       a.S, groups * 16 * kQuads, a.stride,
@@ -588,10 +598,11 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, int64_t index, int c
       },
       [&](int i, f32x4_t f) {
         const int r = i / kQuads, j = i % kQuads * 4;
-        u32x2 hi, lo;
-        split4(f, hi, lo);
-        *reinterpret_cast<u32x2*>(s_hi + r * kPitch + j) = hi;
-        *reinterpret_cast<u32x2*>(s_lo + r * kPitch + j) = lo;
+        u32x2 part[kParts];
+        split4(f, part);
+#pragma unroll
+        for (int d = 0; d < kParts; ++d)
+          *reinterpret_cast<u32x2*>(s_u + d * Lds::kPart + r * kPitch + j) = part[d];
       });
   __syncthreads();
   if (n0 >= a.N) return;
@@ -610,14 +621,17 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, int64_t index, int c
 #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c] = f32x4_t{};
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const int at = (m * 16 + l16) * kPitch + ks * 32 + q * 8;
+    for (int d = 0; d < kParts; ++d) {
 #pragma unroll
-      for (int d = 0; d < (PACK ? 1 : 2); ++d) {
-        const u32x4 u = *reinterpret_cast<const u32x4*>((d == 0 ? s_hi : s_lo) + at);
+      for (int ks = 0; ks < KS; ++ks) {
+        const int at = (m * 16 + l16) * kPitch + ks * 32 + q * 8;
+        const u32x4 u = *reinterpret_cast<const u32x4*>(s_u + d * Lds::kPart + at);
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[c] = mfma(u, wv[ks][c], acc[c]);
       }
+      // the parts one after the other: read together they cost registers, and with
+      // KS == 2 some are spilled (8111 x 2048, rank 64: 22.1 us against 19.0)
+      if (KS == 2) __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -675,24 +689,24 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, int64_t index, int c
 // Block `block` of `blocks`: the columns of a tile fastest, and after the tiles
 // the rows of no selection.  (As further columns of the tiles the copies were on
 // the same XCDs throughout wherever all columns together were a multiple of 8.)
-template <int KS, bool PACK, bool JMAJOR>
+template <int KS, bool JMAJOR>
 __device__ __forceinline__ void expand_block(const ExpandArgs& a, unsigned block, unsigned blocks, char* s_mem) {
   const unsigned ncb = static_cast<unsigned>((a.N + 4 * kCols - 1) / (4 * kCols));
   const unsigned tiles = static_cast<unsigned>(a.num_tiles) * ncb;
   if (block < tiles) {
-    expand<KS, PACK, JMAJOR>(a, block / ncb, static_cast<int>(block % ncb), s_mem);
+    expand<KS, JMAJOR>(a, block / ncb, static_cast<int>(block % ncb), s_mem);
   } else {
     copy_unselected(a, static_cast<int64_t>(block - tiles) * kCopyTokens,
                     static_cast<int64_t>(blocks - tiles) * kCopyTokens);
   }
 }
 
-template <int KS, bool PACK>
+template <int KS>
 __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(KS == 1 ? 3 : 2))) void k_lora_expand(
     ExpandArgs a) {
-  __shared__ __align__(16) char s_mem[ExpandLds<KS, PACK>::kBytes];
+  __shared__ __align__(16) char s_mem[ExpandLds<KS>::kBytes];
   if (!layout_current(a.status, a.generation)) return;
-  expand_block<KS, PACK, false>(a, blockIdx.x, gridDim.x, s_mem);
+  expand_block<KS, false>(a, blockIdx.x, gridDim.x, s_mem);
 }
 
 // --------------------------------------------------------- weight gradients
@@ -717,7 +731,7 @@ struct WeightGradArgs {
   uint32_t generation;
 };
 
-// Rows of u or v that a block holds in LDS at a time: 16 KiB as two bf16 parts.
+// Rows of u or v that a block holds in LDS at a time: 24 KiB as three bf16 parts.
 __host__ __device__ constexpr int staged_rows(int JT) { return 256 / JT; }
 
 // Block: one chunk of an expert's rows, 128 NW columns of x (or g), 16 JT of the
@@ -725,10 +739,11 @@ __host__ __device__ constexpr int staged_rows(int JT) { return 256 / JT; }
 // without a condition (see k_lora_expand).  A lane ends with R's 4 q + i (i < 4)
 // of each 16 and 8 neighbouring columns.
 template <int JT, int NW, int B, bool STREAM>
-__device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile& t, int cb, int jg, uint16_t* s_hi,
-                                            uint16_t* s_lo, int* s_row) {
+__device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile& t, int cb, int jg, uint16_t* s_part,
+                                            int* s_row) {
   constexpr int kStaged = staged_rows(JT);
   constexpr int kPitch = kStaged + 8;
+  constexpr int kPart = JT * 16 * kPitch;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const int l16 = lane & 15, q = lane >> 4;
@@ -769,10 +784,10 @@ __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile&
           const int r = i / (JT * 4), j = i % (JT * 4) * 4;
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
-            uint16_t h, l;
-            split(f[d], h, l);
-            s_hi[(j + d) * kPitch + r] = h;
-            s_lo[(j + d) * kPitch + r] = l;
+            uint16_t part[kParts];
+            split(f[d], part);
+#pragma unroll
+            for (int n = 0; n < kParts; ++n) s_part[n * kPart + (j + d) * kPitch + r] = part[n];
           }
         });
     __syncthreads();
@@ -791,12 +806,11 @@ __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile&
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
           const int at = (j * 16 + l16) * kPitch + r + d * 32 + q * 8;
-          const u32x4 h = *reinterpret_cast<const u32x4*>(s_hi + at);
-          const u32x4 l = *reinterpret_cast<const u32x4*>(s_lo + at);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            acc[c][j] = mfma(h, cv[c], acc[c][j]);
-            acc[c][j] = mfma(l, cv[c], acc[c][j]);
+          for (int n = 0; n < kParts; ++n) {
+            const u32x4 p = *reinterpret_cast<const u32x4*>(s_part + n * kPart + at);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) acc[c][j] = mfma(p, cv[c], acc[c][j]);
           }
         }
       }
@@ -851,11 +865,10 @@ __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile&
 
 // dA, dB and dx in one launch: all need u and v and no more.  The first
 // blocks take the weight gradients, the longer work, the others tiles of dx.
-template <int KS, bool PACK, int JT>
+template <int KS, int JT>
 __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(2))) void k_lora_gradients(
     WeightGradArgs w, ExpandArgs x, unsigned weight_blocks) {
-  constexpr int kElems = JT * 16 * (staged_rows(JT) + 8);
-  constexpr int kW = 4 * kElems, kX = ExpandLds<KS, PACK>::kBytes;
+  constexpr int kW = kParts * JT * 16 * (staged_rows(JT) + 8) * 2, kX = ExpandLds<KS>::kBytes;
   __shared__ __align__(16) char s_mem[kW > kX ? kW : kX];
   extern __shared__ int s_row[];  // a chunk's rows
   if (!layout_current(w.status, w.generation)) return;
@@ -871,16 +884,16 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(2))) voi
     const int jg = at % jgs;
     const Tile t = stored_tile(w.chunks, at / jgs);
     if (t.e < 0) return;
-    uint16_t* const s_hi = reinterpret_cast<uint16_t*>(s_mem);
+    uint16_t* const s_part = reinterpret_cast<uint16_t*>(s_mem);
     auto grad = [&](auto stream) __attribute__((always_inline)) {
       constexpr bool kStream = decltype(stream)::value;
-      if (cb < nca) weight_grad<JT, kWavesPerBlock, 0, kStream>(w, t, cb, jg, s_hi, s_hi + kElems, s_row);
-      else weight_grad<JT, kWavesPerBlock, 1, kStream>(w, t, cb - nca, jg, s_hi, s_hi + kElems, s_row);
+      if (cb < nca) weight_grad<JT, kWavesPerBlock, 0, kStream>(w, t, cb, jg, s_part, s_row);
+      else weight_grad<JT, kWavesPerBlock, 1, kStream>(w, t, cb - nca, jg, s_part, s_row);
     };
     if (w.streamed) grad(std::integral_constant<bool, true>());
     else grad(std::integral_constant<bool, false>());
   } else {
-    expand_block<KS, PACK, true>(x, blockIdx.x - weight_blocks, gridDim.x - weight_blocks, s_mem);
+    expand_block<KS, true>(x, blockIdx.x - weight_blocks, gridDim.x - weight_blocks, s_mem);
   }
 }
 
@@ -978,10 +991,9 @@ unsigned expand_blocks(const ExpandArgs& a) {
 
 hipError_t launch_expand(const ExpandArgs& a, hipStream_t s) {
   const unsigned grid = expand_blocks(a);
-  if (a.R <= 16) k_lora_expand<1, true><<<grid, kBlock, 0, s>>>(a);
-  else if (a.R <= 32) k_lora_expand<1, false><<<grid, kBlock, 0, s>>>(a);
-  else if (a.R <= 64) k_lora_expand<2, false><<<grid, kBlock, 0, s>>>(a);
-  else k_lora_expand<4, false><<<grid, kBlock, 0, s>>>(a);
+  if (a.R <= 32) k_lora_expand<1><<<grid, kBlock, 0, s>>>(a);
+  else if (a.R <= 64) k_lora_expand<2><<<grid, kBlock, 0, s>>>(a);
+  else k_lora_expand<4><<<grid, kBlock, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -989,10 +1001,10 @@ hipError_t launch_gradients(const WeightGradArgs& w, const ExpandArgs& x, const 
   const unsigned wb = static_cast<unsigned>(lora_weight_blocks(g, w.C[0], w.C[1], w.R));
   const unsigned blocks = wb + expand_blocks(x);
   const size_t lds = sizeof(int) << g.chunk_shift;
-  if (w.R <= 16) k_lora_gradients<1, true, 1><<<blocks, kBlock, lds, s>>>(w, x, wb);
-  else if (w.R <= 32) k_lora_gradients<1, false, 2><<<blocks, kBlock, lds, s>>>(w, x, wb);
-  else if (w.R <= 64) k_lora_gradients<2, false, 4><<<blocks, kBlock, lds, s>>>(w, x, wb);
-  else k_lora_gradients<4, false, 4><<<blocks, kBlock, lds, s>>>(w, x, wb);
+  if (w.R <= 16) k_lora_gradients<1, 1><<<blocks, kBlock, lds, s>>>(w, x, wb);
+  else if (w.R <= 32) k_lora_gradients<1, 2><<<blocks, kBlock, lds, s>>>(w, x, wb);
+  else if (w.R <= 64) k_lora_gradients<2, 4><<<blocks, kBlock, lds, s>>>(w, x, wb);
+  else k_lora_gradients<4, 4><<<blocks, kBlock, lds, s>>>(w, x, wb);
   return hipGetLastError();
 }
 

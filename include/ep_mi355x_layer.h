@@ -145,7 +145,7 @@ size_t ep_lora_workspace_bytes(const ep_problem_t* p, const ep_lora_weights_t* w
  * (x is the token matrix, as in ep_expert_gemm), and o(r) = r, or
  * expert_row_src[r] with EP_LORA_SCATTER_ROWS (needs K = 1: each token row
  * has one owner).  The inner product is held in fp32 and enters the outer one
- * as two bf16 parts (16 significand bits); sums are fp32.
+ * unrounded; sums are fp32.
  *   x     bf16, row stride x_row_stride elements (0 = H)
  *   base  bf16, row stride base_row_stride (0 = N); NULL = zeros; may be out
  *         itself (same pointer and stride: the delta is added in place)
@@ -175,7 +175,7 @@ int ep_lora(const ep_problem_t* p, const ep_layout_t* L, const ep_lora_weights_t
  * projection beside the adapter sends to x.  Rows of no selection are treated
  * as ep_lora treats out's.  Every element of grad_a and grad_b is written, 0
  * for an expert without rows.  u and v are held in fp32 and enter the products
- * as two bf16 parts; sums are fp32 in a fixed order.  Row strides are as in
+ * unrounded; sums are fp32 in a fixed order.  Row strides are as in
  * ep_lora (0 = H for x, grad_base and grad_x, N for grad_out), as are the
  * checks. */
 int ep_lora_backward(const ep_problem_t* p, const ep_layout_t* L, const ep_lora_weights_t* w,

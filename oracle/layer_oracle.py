@@ -4,7 +4,7 @@ Plain numpy in float64, one token or one expert at a time, written from the
 formulas and sharing nothing with the HIP kernels.  bf16 inputs arrive as
 float64 values.  The ``*_bound`` results are absolute error bounds per
 element for a kernel that accumulates in fp32, holds the adapters' inner
-products as two bf16 parts and rounds once to its output type.
+products in fp32 and rounds once to its output type.
 """
 from __future__ import annotations
 
@@ -12,7 +12,6 @@ import numpy as np
 
 U32 = 2.0**-24  # half a step of fp32, relative
 UBF = 2.0**-8  # half a step of bf16, relative
-USPLIT = 2.0**-16  # two bf16 parts: half a step of the high one times half a step of the low one
 
 
 def _clean(l):
@@ -158,7 +157,7 @@ def lora(x, a, b, scales, base, rows_of):
         if len(xi) == 0:
             continue
         u = x[xi] @ a[e].T
-        uerr = USPLIT * np.abs(u) + H * U32 * (np.abs(x[xi]) @ np.abs(a[e]).T)
+        uerr = H * U32 * (np.abs(x[xi]) @ np.abs(a[e]).T)
         d = scales[e] * (u @ b[e].T)
         mag = abs(scales[e]) * (np.abs(u) @ np.abs(b[e]).T)
         out[oi] = base[oi] + d
@@ -179,8 +178,8 @@ def lora_backward(go, x, a, b, scales, base, rows_of):
             continue
         s = abs(scales[e])
         u, v = x[xi] @ a[e].T, go[oi] @ b[e]
-        uerr = USPLIT * np.abs(u) + H * U32 * (np.abs(x[xi]) @ np.abs(a[e]).T)
-        verr = USPLIT * np.abs(v) + N * U32 * (np.abs(go[oi]) @ np.abs(b[e]))
+        uerr = H * U32 * (np.abs(x[xi]) @ np.abs(a[e]).T)
+        verr = N * U32 * (np.abs(go[oi]) @ np.abs(b[e]))
         gx[oi] = base[oi] + scales[e] * (v @ a[e])
         bx[oi] = (UBF * np.abs(gx[oi]) + s * (verr @ np.abs(a[e])) +
                   2 * (R + 2) * U32 * s * (np.abs(v) @ np.abs(a[e])) + 2 * U32 * np.abs(base[oi]))

@@ -360,3 +360,77 @@ def test_lora_repeats_graph_and_streams():
     two = step(eager)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(one + two, want + want))
+
+
+def _needs_24_bits(T, E, H, N, R):
+    """Inputs whose u and v are 1 + 2^-10 + 2^-20 and -(1 + 2^-10): in every
+    result those cancel to a multiple of 2^-20, in some without anything
+    larger left.  Each expert has 8 rows of them and zeros else, so that no
+    partial sum needs more than 23 bits, in whatever order it is formed."""
+    ids = torch.arange(T) % E
+    x, go = torch.zeros(T, H), torch.zeros(T, N)
+    a, b = torch.zeros(E, R, H), torch.zeros(E, N, R)
+    for e in range(E):
+        rows = torch.nonzero(ids == e).reshape(-1)
+        at = rows[torch.linspace(0, len(rows) - 1, 8).long()]
+        for t in (x, go):
+            t[at[::2], :3] = torch.tensor([1.0, 2.0**-10, 2.0**-20])
+            t[at[1::2], :3] = torch.tensor([-1.0, -(2.0**-10), 0.0])
+            t[at, 4] = 1.0
+    a[:, 0, :3], a[:, 1, :2], a[:, :2, 8:] = 1.0, -1.0, 1.0
+    b[:, :3, 0], b[:, :2, 1], b[:, 8:, :2] = 1.0, -1.0, 1.0
+    return ids, *(t.to(torch.bfloat16) for t in (x, go, a, b))
+
+
+@pytest.mark.parametrize("T,E", [(24, 3), (2600, 3), (4300, 60)])
+@pytest.mark.parametrize("R", [8, 16, 32, 64, 128])
+def test_lora_inner_products_are_not_rounded(T, E, R):
+    """u and v in the second products with all of fp32's 24 bits: every result
+    is the bf16 rounding of the exact value."""
+    m = ep()
+    H, N = 136, 520
+    ids, x, go, a, b = _needs_24_bits(T, E, H, N, R)
+    L = m.ep_layout(ids[:, None].to(DEV), E, expert_row_src=True)
+    dx, dgo, da, db = (t.to(DEV) for t in (x, go, a, b))
+    got = [m.ep_lora(dx, L, da, db, gather=True, scatter=True)]
+    got += m.ep_lora_backward(dgo, dx, L, da, db, gather=True, scatter=True)
+    rows = [np.nonzero(ids.numpy() == e)[0] for e in range(E)]
+    rows_of = [(r, r) for r in rows]
+    out, _ = LO.lora(f64(x), f64(a), f64(b), np.ones(E), np.zeros((T, N)), rows_of)
+    back = LO.lora_backward(f64(go), f64(x), f64(a), f64(b), np.ones(E), np.zeros((T, H)), rows_of)
+    live = np.flatnonzero(f64(x)[:, 2])
+    assert (out[live][:, 8:] == 2.0**-20).all() and (back[0][0][live][:, 8:] == 2.0**-20).all()
+    assert (back[1][0][:, 0, 4] == 2.0**-18).all() and (back[2][0][:, 4, 0] == 2.0**-18).all()
+    for name, g, want in zip(("out", "grad_x", "grad_a", "grad_b"), got, [out, *(w for w, _ in back)]):
+        want32 = torch.from_numpy(want).to(torch.float32)
+        assert torch.equal(want32.double(), torch.from_numpy(want))  # exact in fp32
+        assert torch.equal(g.cpu(), want32.to(torch.bfloat16)), name
+
+
+@pytest.mark.parametrize("R", [8, 32, 64, 128])
+def test_lora_inner_products_above_the_largest_bf16(R):
+    """u and v between the largest bf16 and the largest fp32 are finite."""
+    m = ep()
+    H = N = 64
+    big, more = float(torch.finfo(torch.bfloat16).max), 1.5 * 2.0**119
+    u = big + more
+    assert big + 2.0**119 < u < torch.finfo(torch.float32).max
+    x = torch.zeros(4, H)
+    x[:, 0], x[:, 1] = big, more
+    x[1] *= -1
+    a, b = torch.zeros(1, R, H), torch.zeros(1, N, R)
+    a[0, 0, :2], a[0, 0, 2:] = 1.0, 2.0**-10
+    b[0, :2, 0], b[0, 2:, 0] = 1.0, 2.0**-10
+    x, a, b = (t.to(torch.bfloat16).to(DEV) for t in (x, a, b))
+    L = m.ep_layout(torch.zeros(4, 1, dtype=torch.int64, device=DEV), 1, expert_row_src=True)
+    out = m.ep_lora(x, L, a, b, gather=True, scatter=True)
+    gx, _, _ = m.ep_lora_backward(x, x, L, a, b, gather=True, scatter=True)
+    want = torch.tensor([u, -u, u, u], device=DEV)[:, None].expand(4, N - 2) * 2.0**-10
+    assert torch.equal(out[:, 2:], want.to(torch.bfloat16)) and torch.equal(gx[:, 2:], want.to(torch.bfloat16))
+    # one row's weight gradients: v x^T and g u^T
+    one = m.ep_layout(torch.zeros(1, 1, dtype=torch.int64, device=DEV), 1, expert_row_src=True)
+    small = torch.full((1, H), 2.0**-12, dtype=torch.bfloat16, device=DEV)
+    _, ga, _ = m.ep_lora_backward(x[:1].clone(), small, one, a, b, gather=True, scatter=True)
+    _, _, gb = m.ep_lora_backward(small, x[:1].clone(), one, a, b, gather=True, scatter=True)
+    want = (torch.tensor(u, device=DEV) * 2.0**-12).to(torch.bfloat16)
+    assert (ga[0, 0] == want).all() and (gb[0, :, 0] == want).all()
