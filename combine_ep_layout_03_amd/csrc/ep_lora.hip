@@ -53,6 +53,8 @@ constexpr int kCols = 128;  // columns of one wave
 constexpr int kXcds = 8;
 constexpr int kMaxSplits = 4;  // splits of a contraction over blocks
 
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
 __device__ __forceinline__ f32x4_t mfma(u32x4 a, u32x4 b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                  __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
@@ -88,6 +90,23 @@ __device__ __forceinline__ void split(float f, uint16_t (&part)[kParts]) {
   part[0] = static_cast<uint16_t>(f == f ? b >> 16 : 0x7fc0u);
   part[1] = finite ? static_cast<uint16_t>(c >> 16) : part[0];
   part[2] = finite ? static_cast<uint16_t>(__float_as_uint(last) >> 16) : part[0];
+}
+
+// Where the other factor is infinite, a part of zero makes NaN of what the formula
+// has infinite: there the second and third part of a value that is not 0 are
+// replaced, if zero, by the smallest denormal with its sign (the matrix
+// instructions take denormals as they are).  To be called by the whole block,
+// after a barrier and before another, for the first `count` elements of each
+// part in LDS.
+__device__ __forceinline__ void fill_parts(uint16_t* s_part, int part_size, int count) {
+  for (int i = threadIdx.x; i < count; i += static_cast<int>(blockDim.x)) {
+    const uint16_t first = s_part[i];
+#pragma unroll
+    for (int d = 1; d < kParts; ++d) {
+      uint16_t& p = s_part[d * part_size + i];
+      if ((first & 0x7fff) != 0 && (p & 0x7fff) == 0) p = (first & 0x8000) | 1;
+    }
+  }
 }
 
 // Column m of the 8 x 8 block held as rows v[0..7] of 8 columns.
@@ -541,7 +560,7 @@ struct ExpandLds {
   static constexpr int kPitch = KS * 32 + 8;
   static constexpr int kStaged = expand_rows(KS);
   static constexpr int kPart = kStaged * kPitch;  // elements of one part
-  static constexpr int kBytes = kParts * kPart * 2 + kStaged * 4;
+  static constexpr int kBytes = kParts * kPart * 2 + kStaged * 4 + kWavesPerBlock * 4;
 };
 
 template <int KS, bool JMAJOR>
@@ -550,6 +569,7 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, int64_t index, int c
   constexpr int kPitch = Lds::kPitch, kStaged = Lds::kStaged;
   uint16_t* const s_u = reinterpret_cast<uint16_t*>(s_mem);
   int* const s_row = reinterpret_cast<int*>(s_mem + kParts * Lds::kPart * 2);
+  int* const s_infinite = s_row + kStaged;  // per wave: is an element of its columns?
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const Tile t = stored_tile(a.tiles, static_cast<int>(index));
@@ -587,6 +607,16 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, int64_t index, int c
       for (int i = 0; i < 8; ++i) wv[ks][i] = v[i];
     }
   }
+  u16x2 largest = {};  // magnitudes of its bits; infinities and NaN are 0x7f80 and more
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        largest = __builtin_elementwise_max(largest, __builtin_bit_cast(u16x2, wv[ks][i][c] & 0x7fff7fffu));
+  const bool infinite = ballot(largest[0] >= 0x7f80 || largest[1] >= 0x7f80) != 0;
+  if (lane == 0) s_infinite[wave] = infinite;
   constexpr int kQuads = KS * 8;  // of a row, the ones past R zeros
   const int groups = (t.nrows + 15) / 16;
   joined_quads(
@@ -605,6 +635,10 @@ __device__ __forceinline__ void expand(const ExpandArgs& a, int64_t index, int c
           *reinterpret_cast<u32x2*>(s_u + d * Lds::kPart + r * kPitch + j) = part[d];
       });
   __syncthreads();
+  if (s_infinite[0] | s_infinite[1] | s_infinite[2] | s_infinite[3]) {  // the whole block
+    fill_parts(s_u, Lds::kPart, groups * 16 * kPitch);
+    __syncthreads();
+  }
   if (n0 >= a.N) return;
 
   // this lane's rows 4 q + i of group m
@@ -740,7 +774,7 @@ __host__ __device__ constexpr int staged_rows(int JT) { return 256 / JT; }
 // of each 16 and 8 neighbouring columns.
 template <int JT, int NW, int B, bool STREAM>
 __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile& t, int cb, int jg, uint16_t* s_part,
-                                            int* s_row) {
+                                            int* s_nan, int* s_row) {
   constexpr int kStaged = staged_rows(JT);
   constexpr int kPitch = kStaged + 8;
   constexpr int kPart = JT * 16 * kPitch;
@@ -752,12 +786,6 @@ __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile&
   const int col = c0 + l16 * 8;
   const int j0 = jg * JT * 16;
 
-  f32x4_t acc[8][JT];
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-#pragma unroll
-    for (int j = 0; j < JT; ++j) acc[c][j] = f32x4_t{};
-
   // the rows' places; lanes past C work on its last 8 columns and store nothing
   for (int r = threadIdx.x; r < t.nrows; r += NW * kWave) s_row[r] = a.map[B] ? a.map[B][t.row0 + r] : t.row0 + r;
   __syncthreads();
@@ -767,54 +795,82 @@ __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile&
     for (int i = 0; i < 8; ++i) v[i] = load_row16<STREAM>(in + s_row[min(r + q * 8 + i, t.nrows - 1)] * a.ld[B]);
   };
   constexpr int kAhead = JT <= 2 ? 2 : 1;  // steps in flight, as registers allow
-  u32x4 v[kAhead][8];
+  f32x4_t acc[8][JT];
+  // Infinities among the rows are found by what they do: where a result is NaN
+  // the block starts again, with no part of zero.
+  for (bool fill = false;; fill = true) {
 #pragma unroll
-  for (int d = 0; d < kAhead; ++d) load_step(32 * d, v[d]);
-  for (int r0 = 0; r0 < t.nrows; r0 += kStaged) {
-    if (r0 > 0) __syncthreads();  // the rows staged before are used up
-    const int staged = min(kStaged, (t.nrows - r0 + 63) / 64 * 64);
-    joined_quads(
-        a.S[B], staged * JT * 4, a.stride,
-        [&](int i) -> const float* {
-          const int r = i / (JT * 4), j = j0 + i % (JT * 4) * 4;
-          if (r0 + r >= t.nrows || j >= R) return nullptr;
-          return a.part[B] + static_cast<int64_t>(t.row0 + r0 + r) * R + j;
-        },
-        [&](int i, f32x4_t f) {
-          const int r = i / (JT * 4), j = i % (JT * 4) * 4;
+    for (int c = 0; c < 8; ++c)
 #pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            uint16_t part[kParts];
-            split(f[d], part);
+      for (int j = 0; j < JT; ++j) acc[c][j] = f32x4_t{};
+    u32x4 v[kAhead][8];
 #pragma unroll
-            for (int n = 0; n < kParts; ++n) s_part[n * kPart + (j + d) * kPitch + r] = part[n];
+    for (int d = 0; d < kAhead; ++d) load_step(32 * d, v[d]);
+    for (int r0 = 0; r0 < t.nrows; r0 += kStaged) {
+      if (r0 > 0) __syncthreads();  // the rows staged before are used up
+      const int staged = min(kStaged, (t.nrows - r0 + 63) / 64 * 64);
+      joined_quads(
+          a.S[B], staged * JT * 4, a.stride,
+          [&](int i) -> const float* {
+            const int r = i / (JT * 4), j = j0 + i % (JT * 4) * 4;
+            if (r0 + r >= t.nrows || j >= R) return nullptr;
+            return a.part[B] + static_cast<int64_t>(t.row0 + r0 + r) * R + j;
+          },
+          [&](int i, f32x4_t f) {
+            const int r = i / (JT * 4), j = i % (JT * 4) * 4;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+              uint16_t part[kParts];
+              split(f[d], part);
+#pragma unroll
+              for (int n = 0; n < kParts; ++n) s_part[n * kPart + (j + d) * kPitch + r] = part[n];
+            }
+          });
+      __syncthreads();
+      if (fill) {
+        fill_parts(s_part, kPart, kPart);
+        __syncthreads();
+      }
+      for (int r = 0; r < staged; r += 32 * kAhead) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+          const int at_row = r0 + r + d * 32;
+          if (at_row + 32 > t.nrows) {  // rows past the chunk are zeros in both operands
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (at_row + q * 8 + i >= t.nrows) v[d][i] = u32x4{0u, 0u, 0u, 0u};
           }
-        });
-    __syncthreads();
-    for (int r = 0; r < staged; r += 32 * kAhead) {
+          u32x4 cv[8];
+          columns(v[d], cv);
+          load_step(at_row + 32 * kAhead, v[d]);
 #pragma unroll
-      for (int d = 0; d < kAhead; ++d) {
-        const int at_row = r0 + r + d * 32;
-        if (at_row + 32 > t.nrows) {  // rows past the chunk are zeros in both operands
+          for (int j = 0; j < JT; ++j) {
+            const int at = (j * 16 + l16) * kPitch + r + d * 32 + q * 8;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (at_row + q * 8 + i >= t.nrows) v[d][i] = u32x4{0u, 0u, 0u, 0u};
-        }
-        u32x4 cv[8];
-        columns(v[d], cv);
-        load_step(at_row + 32 * kAhead, v[d]);
+            for (int n = 0; n < kParts; ++n) {
+              const u32x4 p = *reinterpret_cast<const u32x4*>(s_part + n * kPart + at);
 #pragma unroll
-        for (int j = 0; j < JT; ++j) {
-          const int at = (j * 16 + l16) * kPitch + r + d * 32 + q * 8;
-#pragma unroll
-          for (int n = 0; n < kParts; ++n) {
-            const u32x4 p = *reinterpret_cast<const u32x4*>(s_part + n * kPart + at);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) acc[c][j] = mfma(p, cv[c], acc[c][j]);
+              for (int c = 0; c < 8; ++c) acc[c][j] = mfma(p, cv[c], acc[c][j]);
+            }
           }
         }
       }
     }
+    if (fill) break;
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int j = 0; j < JT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += acc[c][j][i];
+    const bool nan = ballot(sum != sum) != 0;
+    if (lane == 0) s_nan[wave] = nan;
+    __syncthreads();  // and the rows staged last are used up
+    int again = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) again |= s_nan[i];
+    if (again == 0) break;  // the whole block
   }
 
   const bool whole = t.slot < 0;
@@ -868,7 +924,8 @@ __device__ __forceinline__ void weight_grad(const WeightGradArgs& a, const Tile&
 template <int KS, int JT>
 __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(2))) void k_lora_gradients(
     WeightGradArgs w, ExpandArgs x, unsigned weight_blocks) {
-  constexpr int kW = kParts * JT * 16 * (staged_rows(JT) + 8) * 2, kX = ExpandLds<KS>::kBytes;
+  constexpr int kParted = kParts * JT * 16 * (staged_rows(JT) + 8) * 2;
+  constexpr int kW = kParted + kWavesPerBlock * 4, kX = ExpandLds<KS>::kBytes;
   __shared__ __align__(16) char s_mem[kW > kX ? kW : kX];
   extern __shared__ int s_row[];  // a chunk's rows
   if (!layout_current(w.status, w.generation)) return;
@@ -885,10 +942,11 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(2))) voi
     const Tile t = stored_tile(w.chunks, at / jgs);
     if (t.e < 0) return;
     uint16_t* const s_part = reinterpret_cast<uint16_t*>(s_mem);
+    int* const s_nan = reinterpret_cast<int*>(s_mem + kParted);
     auto grad = [&](auto stream) __attribute__((always_inline)) {
       constexpr bool kStream = decltype(stream)::value;
-      if (cb < nca) weight_grad<JT, kWavesPerBlock, 0, kStream>(w, t, cb, jg, s_part, s_row);
-      else weight_grad<JT, kWavesPerBlock, 1, kStream>(w, t, cb - nca, jg, s_part, s_row);
+      if (cb < nca) weight_grad<JT, kWavesPerBlock, 0, kStream>(w, t, cb, jg, s_part, s_nan, s_row);
+      else weight_grad<JT, kWavesPerBlock, 1, kStream>(w, t, cb - nca, jg, s_part, s_nan, s_row);
     };
     if (w.streamed) grad(std::integral_constant<bool, true>());
     else grad(std::integral_constant<bool, false>());

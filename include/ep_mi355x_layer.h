@@ -145,7 +145,8 @@ size_t ep_lora_workspace_bytes(const ep_problem_t* p, const ep_lora_weights_t* w
  * (x is the token matrix, as in ep_expert_gemm), and o(r) = r, or
  * expert_row_src[r] with EP_LORA_SCATTER_ROWS (needs K = 1: each token row
  * has one owner).  The inner product is held in fp32 and enters the outer one
- * unrounded; sums are fp32.
+ * unrounded; sums are fp32.  Infinities and NaN go where the formula takes
+ * them (an inner product below 2^-133 counts as 0 beside an infinity).
  *   x     bf16, row stride x_row_stride elements (0 = H)
  *   base  bf16, row stride base_row_stride (0 = N); NULL = zeros; may be out
  *         itself (same pointer and stride: the delta is added in place)

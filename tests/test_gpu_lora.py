@@ -434,3 +434,50 @@ def test_lora_inner_products_above_the_largest_bf16(R):
     _, _, gb = m.ep_lora_backward(small, x[:1].clone(), one, a, b, gather=True, scatter=True)
     want = (torch.tensor(u, device=DEV) * 2.0**-12).to(torch.bfloat16)
     assert (ga[0, 0] == want).all() and (gb[0, :, 0] == want).all()
+
+
+def _formula(x, go, a, b, rows):
+    """The four results of one expert's rows, in float64 and without a matrix
+    product of a library, so that infinities go as the formulas have them."""
+    with np.errstate(invalid="ignore"):
+        u = (x[rows][:, None, :] * a[None]).sum(2)
+        v = (go[rows][:, :, None] * b[None]).sum(1)
+        out, gx = (u[:, None, :] * b[None]).sum(2), (v[:, :, None] * a[None]).sum(1)
+        ga = (v[:, :, None] * x[rows][:, None, :]).sum(0)
+        gb = (go[rows][:, :, None] * u[:, None, :]).sum(0)
+    return out, gx, ga, gb
+
+
+@pytest.mark.parametrize("where", ["a", "b", "x", "go", "a and x", "b and go"])
+@pytest.mark.parametrize("R", [8, 16, 24, 64, 128])
+@pytest.mark.parametrize("T", [9, 700])
+def test_lora_infinite_factors_of_the_second_products(T, R, where):
+    """An infinity in B, A, x or grad_out meets u and v whose bf16 parts may be
+    zero (small integers): the result is the formula's infinity, NaN only
+    where the formula has it (0 times infinity, infinities of both signs), and
+    what the infinity does not reach is as without it."""
+    m = ep()
+    H, N = 72, 136
+    g = torch.Generator().manual_seed(R + T)
+    ints = lambda *s: torch.randint(1, 4, s, generator=g).float()  # noqa: E731  positive: u and v are not 0
+    x, go, a, b = ints(T, H), ints(T, N), ints(1, R, H), ints(1, N, R)
+    a[0, R // 2] *= -1  # some u and dx terms negative
+    b[0, :, 1] = 0.0  # v of it is 0
+    for name in where.split(" and "):
+        t = dict(a=a[0], b=b[0], x=x, go=go)[name]
+        t[-1, 5], t[0, t.shape[1] - 1] = float("inf"), float("-inf")
+    x, go, a, b = (t.to(torch.bfloat16) for t in (x, go, a, b))
+    L = m.ep_layout(torch.zeros(T, 1, dtype=torch.int64, device=DEV), 1, expert_row_src=True)
+    d = [t.to(DEV) for t in (x, go, a, b)]
+    got = [m.ep_lora(d[0], L, d[2], d[3], gather=True, scatter=True)]
+    got += m.ep_lora_backward(d[1], d[0], L, d[2], d[3], gather=True, scatter=True)
+    want = _formula(f64(x), f64(go), f64(a[0]), f64(b[0]), np.arange(T))
+    for name, v, w in zip(("out", "grad_x", "grad_a", "grad_b"), got, want):
+        v = f64(v).reshape(w.shape)
+        assert np.array_equal(np.isnan(v), np.isnan(w)), name
+        inf = np.isinf(w)
+        assert np.array_equal(np.isinf(v), inf) and np.array_equal(v[inf], w[inf]), name
+        # sums of integers, exact in fp32: below 2^24 but for the gradients of many rows
+        fine = np.isfinite(w)
+        assert (np.abs(v[fine] - w[fine]) <= (LO.UBF + 2 * T * LO.U32) * np.abs(w[fine]) + T * 2.0**-100).all(), name
+    assert any(np.isinf(w).any() for w in want)
