@@ -607,7 +607,7 @@ __global__ __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) void
       const float u = unordered(x & ~kLowMask), v = unordered(y & ~kLowMask);
       float tol = 0x1p-22f * (1u << kLow) * fabsf(v) + 1e-37f;
       if (BY == kByScore) tol += err(u) + err(v);
-      return u - v <= tol;
+      return !(u - v > tol);  // two of +inf, whose difference is NaN, are equal
     };
     const uint64_t before = lanemask_lt() & ~((1ull << (tok * LPT)) - 1);  // the token's lanes below this one
     auto drop_head = [&](bool mine) __attribute__((always_inline)) {

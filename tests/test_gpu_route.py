@@ -333,3 +333,25 @@ def test_route_graph_and_streams():
     got_l = step(l)
     torch.cuda.synchronize()
     assert all(torch.equal(a, c) for a, c in zip(got_l + got_o, want_l + want_o))
+
+
+@pytest.mark.parametrize("E", [64, 100, 256, 300, 1000])
+@pytest.mark.parametrize("copies", [1, 160])
+def test_route_infinite_biases(E, copies):
+    """Several experts with a bias of +inf have equal selection values: the
+    lowest indices go first, whichever lanes hold them, alone, beside finite
+    ones, and in groups."""
+    l = _logits(14, E, torch.float32, E)
+    rng = np.random.default_rng(E)
+    for some in ([1, 4], [E - 1, E - 2, 5, 8, 3], sorted(rng.choice(E, 24, replace=False)), range(E)):
+        b = _bias(E, 5)
+        b[torch.tensor(list(some))] = float("inf")
+        b[0] = float("nan")
+        b[2] = float("-inf")
+        for K in (1, 4, 8, 32):
+            _check(l, K, "sigmoid", bias=b, copies=copies)
+            _check(l.to(torch.bfloat16), K, "softmax", bias=b, renorm=True, copies=copies)
+        if E % 4 == 0:
+            for gtop in (1, 2):
+                _check(l, 3, "sigmoid", b, 4, 2, gtop, copies=copies)
+                _check(l, 8, "softmax", b, E // (4 if E <= 256 else 20), 3, gtop, copies=copies)
