@@ -498,13 +498,14 @@ __global__ __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) void
       }
       if constexpr (BY == kByScore) bmax = over_token<LPT>(bmax, Max());
     }
-    // bounds on the error of a value, score + bias, and of a sum of two
+    // bounds on the error of a value, score + bias, and of half a sum of two (half
+    // of what two errors and the sum's rounding add up to)
     const float cap = a.sigmoid ? 0x1p-21f : 0x1p-18f;
     auto err = [&](float v) {
       return fminf(cap, 0x1p-16f * (fabsf(v) + bmax)) + 0x1p-22f * fabsf(v) + 1e-37f;
     };
     auto err2 = [&](float v) {
-      return fminf(2.0f * cap, 0x1p-16f * (fabsf(v) + 2.0f * bmax)) + 0x1p-22f * (fabsf(v) + 4.0f * bmax) + 2e-37f;
+      return fminf(cap, 0x1p-16f * (fabsf(v) + bmax)) + (0x1p-22f * fabsf(v) + 0x1p-21f * bmax) + 1e-37f;
     };
 
     uint64_t open = ~0ull;
@@ -518,6 +519,10 @@ __global__ __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) void
       // keeps the groups on different banks
       const int P = a.G * 4 <= LPT && a.gsize % 4 == 0 ? 4 : a.G * 2 <= LPT && a.gsize % 2 == 0 ? 2 : 1;
       const int sub = g % P;
+      // a group's value; of two, half the sum: two finite biases' may overflow
+      auto value = [&](float m1, float m2) {
+        return a.gtop == 1 ? m1 : m2 > kNegInf ? 0.5f * m1 + 0.5f * m2 : 0.5f * m1;
+      };
       for (int q = g / P; q < a.G; q += LPT / P) {
         float m1 = kNegInf, m2 = kNegInf;
         int at = (q * P) % a.gsize;
@@ -535,7 +540,7 @@ __global__ __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) void
           m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
           m1 = fmaxf(m1, o1);
         }
-        if (sub == 0) gvf[q] = (a.gtop == 2 && m2 > kNegInf) ? m1 + m2 : m1;
+        if (sub == 0) gvf[q] = value(m1, m2);
       }
       lds_sync();
       float last, next;

@@ -355,3 +355,25 @@ def test_route_infinite_biases(E, copies):
             for gtop in (1, 2):
                 _check(l, 3, "sigmoid", b, 4, 2, gtop, copies=copies)
                 _check(l, 8, "softmax", b, E // (4 if E <= 256 else 20), 3, gtop, copies=copies)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("copies", [1, 160])
+def test_route_group_values_past_fp32(sign, copies):
+    """Group values that are sums of two finite biases and overflow fp32: the
+    groups are still told apart, and differ from one without experts."""
+    E, G = 64, 8
+    l = _logits(15, E, torch.float32, 8)
+    base = sign * torch.tensor([2.0e38, 2.2e38, 3.0e38, 2.9e38, 1.8e38, 3.3e38, 2.5e38, 3.4e38])
+    b = base.repeat_interleave(E // G)
+    for TG in (1, 3, 7):
+        _check(l, 6, "sigmoid", b, G, TG, 2, copies=copies)
+        _check(l, 6, "softmax", b, G, TG, 2, copies=copies)
+    b[8:16] = float("-inf")  # a group without an expert to choose
+    b[16:24] = float("nan")
+    for TG in (2, 6, 8):
+        _check(l, 6, "sigmoid", b, G, TG, 2, copies=copies)
+    b[24] = float("inf")
+    _check(l, 6, "sigmoid", b, G, 2, 2, copies=copies)
+    b = torch.full((E,), sign * 3.0e38)  # all equal, all past fp32
+    _check(l, 6, "sigmoid", b, G, 3, 2, copies=copies)
