@@ -61,7 +61,7 @@ __device__ __forceinline__ f32x4_t mfma(u32x4 a, u32x4 b, f32x4_t c) {
 }
 
 __device__ __forceinline__ u32x4 load16(const uint16_t* p) { return *reinterpret_cast<const u32x4*>(p); }
-// STREAM: non-temporal, for the last read of rows that the caches could not keep.
+// STREAM: non-temporal, for the only read of rows that the caches could not keep.
 template <bool STREAM>
 __device__ __forceinline__ u32x4 load_row16(const uint16_t* p) {
   return STREAM ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)) : load16(p);
@@ -758,7 +758,7 @@ struct WeightGradArgs {
   int64_t slot_size;  // R * (H + N)
   const float* scales;
   int R, E, shift;
-  bool streamed;
+  bool streamed[2];
   const int32_t* chunks;
   const int32_t* counts;
   int32_t* status;
@@ -948,7 +948,8 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(2))) voi
       if (cb < nca) weight_grad<JT, kWavesPerBlock, 0, kStream>(w, t, cb, jg, s_part, s_nan, s_row);
       else weight_grad<JT, kWavesPerBlock, 1, kStream>(w, t, cb - nca, jg, s_part, s_nan, s_row);
     };
-    if (w.streamed) grad(std::integral_constant<bool, true>());
+    // (KS == 4 is a rank above 64, whose rows are never streamed)
+    if (KS < 4 && w.streamed[cb < nca ? 0 : 1]) grad(std::integral_constant<bool, KS < 4>());
     else grad(std::integral_constant<bool, false>());
   } else {
     expand_block<KS, true>(x, blockIdx.x - weight_blocks, gridDim.x - weight_blocks, s_mem);
@@ -1088,12 +1089,19 @@ ShrinkArgs shrink_args(const LoraArgs& a, const LoraGeom& g) {
 // the last time here, they then make room for what is: the shrink of 8111 x 7168
 // takes 27 us against 32, of 8192 x 4096 (64 MB) 19 against 21, while a caller's
 // second use of 2048 x 7168 (29 MB) would cost 18 against 14; the weight
-// gradients of 16,384 x 4096 + 2048 and the shrink before the next call's 122 us
-// against 127, of 2048 x 4096 + 4096 27.5 against 25.
-bool streamed(const LoraArgs& a, int64_t columns) {
+// gradients of 16,384 x 4096 + 2048 and the shrink before the next call's 129 us
+// against 133, of 2048 x 4096 + 4096 27.5 against 25.
+bool large_rows(const LoraArgs& a, int64_t columns) {
   const int64_t rows = a.T * a.K;
   return rows * columns * 2 >= (64 << 20);
 }
+
+// Is a row of x read once by a kernel that reads all of them?  Not where its K
+// selections gather it, each into the tile of another expert: streamed, 4096
+// tokens x 4096, K = 4, rank 32 took 32 us against 26 (shrink), 8192 tokens x
+// 7168, K = 8, rank 16 178 against 145, and their weight gradients (8192 x 4096
+// + 2048, K = 4) 118 against 110.
+bool x_read_once(const LoraArgs& a) { return !a.xmap || a.K == 1; }
 
 ExpandArgs expand_args(const LoraArgs& a, const LoraGeom& g) {
   ExpandArgs x = {};
@@ -1190,7 +1198,7 @@ hipError_t launch_lora(const LoraArgs& a, const LoraGeom& g, hipStream_t s) {
   u.C = a.H;
   u.part = a.u;
   u.S = g.split_x;
-  u.streamed = streamed(a, a.H);
+  u.streamed = x_read_once(a) && large_rows(a, a.H);
   const hipError_t err = launch_shrink(u, nullptr, g, s);
   if (err != hipSuccess) return err;
   ExpandArgs x = expand_args(a, g);
@@ -1224,7 +1232,10 @@ hipError_t launch_lora_backward(const LoraArgs& a, const LoraGeom& g, hipStream_
   w.R = a.R;
   w.E = a.E;
   w.shift = g.chunk_shift;
-  w.streamed = streamed(a, a.H + a.N);
+  // above rank 64 two groups of blocks, one for each half of R, read the rows:
+  // rank 128, 16,384 x 4096 + 2048, with the shrink 330 us streamed, 324 not
+  w.streamed[1] = a.R <= 64 && large_rows(a, a.H + a.N);
+  w.streamed[0] = w.streamed[1] && x_read_once(a);
   w.chunks = a.chunks;
   w.counts = a.counts;
   w.status = a.status;
