@@ -1170,7 +1170,11 @@ LoraGeom lora_geom(int64_t rows, int E, int H, int N, int R, bool backward) {
     // Chunks of an expert's rows, about 32 of all rows: more cost partial
     // gradients, fewer leave CUs idle (65,536 rows x 2048 -> 2048, rank 32, join
     // included: 161 us; with 64 chunks 161, with 16 210.  16,384 x 4096: 78, 86
-    // and 80.  509 rows: 12 us with chunks of 64, 128 or 256 rows).
+    // and 80.  509 rows: 12 us with chunks of 64, 128 or 256 rows).  A chunk has
+    // 4096 rows at most, as its list of rows lies in LDS (16 KiB, so that two
+    // blocks fit a CU): above 131,072 rows there are more, one for 4096 rows, and
+    // the partial gradients grow with the rows (524,288 rows, rank 64, 7168 ->
+    // 2048: 256 of 2.4 MB).
     g.chunk_shift = 7;
     while (g.chunk_shift < 12 && (static_cast<int64_t>(32) << g.chunk_shift) < rows) ++g.chunk_shift;
     g.max_chunks = up8((rows >> g.chunk_shift) + used);

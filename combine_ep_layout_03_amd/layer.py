@@ -254,7 +254,8 @@ def _lora_workspace(T, H, K, E, G, A, flags, R, N, wflags, backward) -> int:
 
 def ep_lora_workspace_bytes(layout: Layout, hidden: int, n_out: int, rank: int, backward: bool = False) -> int:
     """Bytes of workspace ``ep_lora`` (or ``ep_lora_backward``) needs on this
-    layout; 0 if it would refuse the sizes."""
+    layout; 0 if it would refuse the sizes.  The backward pass's holds partial
+    gradients and grows with the rows above 131,072 (the C header has the rule)."""
     layout, _ = _resolve(layout)
     return _lora_workspace(layout.num_tokens, int(hidden), layout.topk, layout.num_experts, layout.num_groups,
                            layout.expert_alignment, 0, int(rank), int(n_out), 0, int(backward))

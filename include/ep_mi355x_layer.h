@@ -134,7 +134,9 @@ typedef struct ep_lora_weights {
 } ep_lora_weights_t;
 
 /* Bytes of device workspace ep_lora (backward == 0) or ep_lora_backward (1)
- * needs for this problem; 0 if ep_lora would refuse it.  Host only. */
+ * needs for this problem; 0 if ep_lora would refuse it.  Host only.  The backward
+ * pass keeps partial gradients of R * (H + N) fp32 each: up to 64 for T * K (and
+ * padding) up to 131,072 rows, one for 2048 rows above. */
 size_t ep_lora_workspace_bytes(const ep_problem_t* p, const ep_lora_weights_t* w, int32_t backward);
 
 /* out = base + scales[e] * (x A_e^T) B_e^T over the expert-major segments: for

@@ -481,3 +481,22 @@ def test_lora_infinite_factors_of_the_second_products(T, R, where):
         fine = np.isfinite(w)
         assert (np.abs(v[fine] - w[fine]) <= (LO.UBF + 2 * T * LO.U32) * np.abs(w[fine]) + T * 2.0**-100).all(), name
     assert any(np.isinf(w).any() for w in want)
+
+
+@pytest.mark.parametrize("T,K,R", [(135_000, 1, 8), (140_000, 1, 72), (67_000, 2, 24)])
+def test_lora_backward_more_rows_than_32_chunks_hold(T, K, R):
+    """More than 131,072 rows, where the weight gradients' chunks have reached
+    4096 rows and their number grows.  Small integers, every sum exact: the
+    gradients are the bf16 roundings of the exact values."""
+    E, H, N = 4, 24, 16
+    ids = _ids(T, K, E, T, none=0.02)
+    assert (ids >= 0).sum() > 131_072
+    c = Case(ids, E, H, N, R, True, K == 1, seed=R, ints=True)
+    gx, ga, gb, want = c.backward()
+    for e, (xi, oi) in enumerate(c.rows_of):  # no sum of magnitudes leaves fp32's whole numbers
+        u, v = f64(c.x)[xi] @ f64(c.a)[e].T, f64(c.go)[oi] @ f64(c.b)[e]
+        assert max((np.abs(v).T @ np.abs(f64(c.x)[xi])).max(), (np.abs(f64(c.go)[oi]).T @ np.abs(u)).max()) < 2**24
+    sel = torch.from_numpy(c.selected)
+    for name, g, (v, _) in zip("xab", (gx, ga, gb), want):
+        v = torch.from_numpy(v).to(torch.float32).to(torch.bfloat16)
+        assert torch.equal(g.cpu()[sel] if name == "x" else g.cpu(), v[sel] if name == "x" else v), name
