@@ -273,3 +273,52 @@ def test_workspace_covers_every_split_of_the_rows():
         assert sum(chunks) <= (rows >> shift) + min(rows, E)
         u_and_v = _geom(rows, 1, E, 64, 64, 8, backward=1) - 2 * (rows >> shift) * 8 * 128 * 4
         assert u_and_v >= 2 * rows * 8 * 4
+
+
+def _parts(rows, E, H, N, R):
+    """Bytes of the backward workspace's parts as the kernels index them, for
+    H and N below 512 (contractions are not split): 16 a result tile and
+    weight-gradient chunk, R fp32 a row of u and of v, R * (H + N) a slot."""
+    used, up8 = min(rows, E), lambda n: (n + 7) // 8 * 8
+    tile = 7 if R <= 64 else 6
+    while tile > 4 and rows >> tile < 192:
+        tile -= 1
+    chunk = 7
+    while chunk < 12 and 32 << chunk < rows:
+        chunk += 1
+    return tile, chunk, dict(tiles=16 * up8((rows >> tile) + used), chunks=16 * up8((rows >> chunk) + used),
+                             u=rows * R * 4, v=rows * R * 4, slots=2 * (rows >> chunk) * R * (H + N) * 4)
+
+
+@pytest.mark.parametrize("R", [8, 64, 128])
+def test_workspace_parts_to_the_byte(R):
+    """The library reserves each part in full, at sizes on both sides of every
+    step, and each part holds what a split of the rows over experts puts there."""
+    import random
+
+    rng = random.Random(R)
+    sizes = [1, 2, 127, 128, 129, 4095, 4096, 4097, 8191, 8192, 131_071, 131_072, 131_073, 300_000]
+    sizes += [rng.randint(1, 5000) for _ in range(60)] + [rng.randint(5000, 400_000) for _ in range(30)]
+    for rows in sizes:
+        E, H, N = rng.randint(1, 40), 8 * rng.randint(1, 63), 8 * rng.randint(1, 63)
+        tile, chunk, parts = _parts(rows, E, H, N, R)
+        assert _geom(rows, 1, E, H, N, R) == sum(parts.values()), (rows, E, H, N, parts)
+        for even in (False, True):
+            if even:  # every expert just past a whole number of chunks, as far as the rows go
+                counts, left = [], rows
+                for _ in range(E):
+                    n = min(left, ((rows // E >> chunk) << chunk) + 1)
+                    counts.append(n)
+                    left -= n
+                counts[-1] += left
+            else:
+                cuts = sorted(rng.randint(0, rows) for _ in range(E - 1))
+                counts = [b - a for a, b in zip([0, *cuts], [*cuts, rows])]
+            assert sum(counts) == rows
+            up = lambda c, s: (c + (1 << s) - 1) >> s  # noqa: E731
+            many = sum(up(c, chunk) for c in counts if up(c, chunk) > 1)
+            assert 16 * sum(up(c, tile) for c in counts) <= parts["tiles"]
+            assert 16 * sum(up(c, chunk) for c in counts) <= parts["chunks"]
+            assert many * R * (H + N) * 4 <= parts["slots"]
+    # padding to an alignment takes rows too
+    assert _geom(100, 2, 8, 64, 64, R, A=16) == sum(_parts(200 + 8 * 15, 8, 64, 64, R)[2].values())
