@@ -32,15 +32,18 @@
 // Measured (a plain copy: 4.98 TB/s):
 //     16,384 rows, 4096 -> 2048, rank 32, 64 experts, in expert order
 //       forward   shrink 32 us (x 134 MB), expand 36 us (base and out 134 MB)
-//       backward  shrink 55 us (x and g 201 MB), gradients 68 us (x and g again,
+//       backward  shrink 55 us (x and g 201 MB), gradients 75 us (x and g again,
 //                 and dx, 134 MB), join 5 us
+//     the same at rank 128: backward shrink 148 us, gradients 190 us, join 9 us
 //     8111 tokens, 7168 -> 2048, rank 64, 10% without an adapter
-//       forward   shrink 27 us (x 105 MB), expand 18 us (base and out 66 MB)
-//     61 tokens, 4096 -> 4096, rank 16: 5.1 + 5.5 us; 509 tokens, rank 8, backward:
-//       7.0 + 8.6 + 3.5 us.  Launch, tile search and three dependent loads are
-//       most of these.
-// The matrix units are busy for at most a tenth of a kernel's time: memory's
-// latency and rate bound the long ones.
+//       forward   shrink 27 us (x 105 MB), expand 19 us (base and out 66 MB);
+//                 rank 128: 49 and 29 us
+//     61 tokens, 4096 -> 4096, rank 16, 48 adapters: 5.7 + 5.5 us; 509 tokens,
+//       rank 8, backward: 7.2 + 9.9 + 4.0 us.  Launch, tile search and three
+//       dependent loads are most of these.
+// At their peak rate the matrix units need a tenth of a kernel's time up to rank
+// 32 and a fifth at rank 128: memory's latency and rate bound the long ones,
+// above rank 64 the L2's too, as a block keeps few rows of each matrix it reads.
 #include <type_traits>
 
 #include "ep_layer.h"
@@ -1154,9 +1157,9 @@ LoraGeom lora_geom(int64_t rows, int E, int H, int N, int R, bool backward) {
     return n;
   };
   // The result's tiles: the longest of which the rows alone, in one expert, fill
-  // three quarters of the CUs (rank 64, 8111 x 2048: 20.9 us with 128 rows, 22.9
-  // with 64, 26.9 with 32; 2048 x 2048: 8.5 with 32, 10.9 with 16; rank 16, 1024 x
-  // 4096: 8.0 with 32, 8.8 with 16)
+  // three quarters of the CUs (rank 64, 8111 x 2048: 19.0 us with 128 rows, 19.4
+  // with 64, 22.5 with 32; 2048 x 2048: 8.6 with 32, 11.4 with 16; rank 16, 1024 x
+  // 4096: 8.5 with 32, 9.1 with 16)
   const int64_t col_blocks = ((backward ? H : N) + 4 * kCols - 1) / (4 * kCols);
   g.expand_shift = R <= 64 ? 7 : 6;
   while (g.expand_shift > 4 && (rows >> g.expand_shift) * col_blocks < 192) --g.expand_shift;
@@ -1169,8 +1172,9 @@ LoraGeom lora_geom(int64_t rows, int E, int H, int N, int R, bool backward) {
     g.v_bytes = static_cast<size_t>(up16(g.split_g * rows * R * 4));
     // Chunks of an expert's rows, about 32 of all rows: more cost partial
     // gradients, fewer leave CUs idle (65,536 rows x 2048 -> 2048, rank 32, join
-    // included: 161 us; with 64 chunks 161, with 16 210.  16,384 x 4096: 78, 86
-    // and 80.  509 rows: 12 us with chunks of 64, 128 or 256 rows).  A chunk has
+    // included, in four experts: 159 us; with 64 chunks 151, with 16 207; in 64
+    // experts 150, 176 and 150.  16,384 x 4096 + 2048: 78, 88 and 78, and 80, 95
+    // and 79.  509 rows: 13 us with chunks of 128 rows, 12 with 64, 15 with 256).  A chunk has
     // 4096 rows at most, as its list of rows lies in LDS (16 KiB, so that two
     // blocks fit a CU): above 131,072 rows there are more, one for 4096 rows, and
     // the partial gradients grow with the rows (524,288 rows, rank 64, 7168 ->

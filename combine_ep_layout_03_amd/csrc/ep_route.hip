@@ -768,7 +768,10 @@ __global__ __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) void
 // Lane g of a token holds selections g and g + LPT; the gradient's row is put
 // together in LDS and written whole.  65,536 tokens x 256, top-8, sigmoid
 // renormalised, fp32: 19.6 us, 140 MB, much of it still in the memory-side cache;
-// the vector units issue for half of that time.  4096 x 64, softmax: 5.2 us.
+// the vector units issue for half of that time.  4096 x 64, softmax: 5.2 us.  The
+// dense gradient (softmax, not renormalised) passes over a row three times, an
+// element a lane: 65,536 x 256 60 us in fp32, 42 in bf16, two to three times its
+// bytes.
 template <int LPT, typename LT>
 __global__ __launch_bounds__(kWave) void k_route_backward(RouteArgs a, int cap) {
   extern __shared__ float s_row[];  // [64 / LPT][cap]

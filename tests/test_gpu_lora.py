@@ -483,7 +483,7 @@ def test_lora_infinite_factors_of_the_second_products(T, R, where):
     assert any(np.isinf(w).any() for w in want)
 
 
-@pytest.mark.parametrize("T,K,R", [(135_000, 1, 8), (140_000, 1, 72), (67_000, 2, 24)])
+@pytest.mark.parametrize("T,K,R", [(135_000, 1, 8), (140_000, 1, 72), (67_000, 2, 24), (136_000, 1, 64)])
 def test_lora_backward_more_rows_than_32_chunks_hold(T, K, R):
     """More than 131,072 rows, where the weight gradients' chunks have reached
     4096 rows and their number grows.  Small integers, every sum exact: the
