@@ -1,7 +1,8 @@
 """MoE token dispatch / combine for one MI355X (gfx950).
 
-A thin binding over the C ABI in include/ep_mi355x.h (here) and
-include/ep_mi355x_layer.h (layer.py): each function checks
+A thin binding over the C ABI in include/ep_mi355x.h (here),
+include/ep_mi355x_layer.h (layer.py) and include/ep_mi355x_expert.h
+(expert.py): each function checks
 that the torch tensors it is handed are contiguous device tensors of the
 right dtype and shape, allocates outputs with torch (device memory is the
 only thing torch provides here), and calls the library entry point of the
@@ -17,6 +18,11 @@ import torch
 
 from . import _lib
 from ._lib import (  # noqa: F401
+    EP_ACT_GELU,
+    EP_ACT_GELU_TANH,
+    EP_ACT_NONE,
+    EP_ACT_RELU,
+    EP_ACT_SILU,
     EP_COMBINE_FLAT,
     EP_COMBINE_GROUPED,
     EP_FORMAT_BF16,
@@ -61,6 +67,12 @@ __all__ = [
     "ep_lora_workspace_bytes",
     "ep_lora",
     "ep_lora_backward",
+    "ep_expert_linear",
+    "ep_expert_linear_workspace_bytes",
+    "ep_expert_linear_backward",
+    "ep_balance_workspace_bytes",
+    "ep_balance_loss",
+    "ep_balance_loss_backward",
     "ep_strerror",
     "EPError",
 ]
@@ -617,4 +629,12 @@ from .layer import (  # noqa: E402  (built on the helpers above)
     ep_lora_workspace_bytes,
     ep_route,
     ep_route_backward,
+)
+from .expert import (  # noqa: E402
+    ep_balance_loss,
+    ep_balance_loss_backward,
+    ep_balance_workspace_bytes,
+    ep_expert_linear,
+    ep_expert_linear_backward,
+    ep_expert_linear_workspace_bytes,
 )

@@ -1,5 +1,5 @@
-"""ctypes loader for the HIP library and the C structs of include/ep_mi355x.h
-and include/ep_mi355x_layer.h.
+"""ctypes loader for the HIP library and the C structs of include/ep_mi355x.h,
+include/ep_mi355x_layer.h and include/ep_mi355x_expert.h.
 
 There is no fallback: if the library is not built, loading raises.
 """
@@ -54,6 +54,11 @@ EP_SCORE_SIGMOID = 1
 EP_LOGITS_FP32 = 0
 EP_LOGITS_BF16 = 1
 EP_LORA_SCATTER_ROWS = 1
+EP_ACT_NONE = 0
+EP_ACT_RELU = 1
+EP_ACT_SILU = 2
+EP_ACT_GELU = 3
+EP_ACT_GELU_TANH = 4
 
 EXPORTS = (
     "ep_fp8_row_bytes",
@@ -72,6 +77,12 @@ EXPORTS = (
     "ep_lora_workspace_bytes",
     "ep_lora",
     "ep_lora_backward",
+    "ep_expert_linear",
+    "ep_expert_linear_workspace_bytes",
+    "ep_expert_linear_backward",
+    "ep_balance_workspace_bytes",
+    "ep_balance_loss",
+    "ep_balance_loss_backward",
 )
 
 
@@ -133,6 +144,28 @@ class LoraWeights(ctypes.Structure):
     ]
 
 
+class Linear(ctypes.Structure):
+    _fields_ = [
+        ("w", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("n_out", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("gated", ctypes.c_int32),
+    ]
+
+
+class Balance(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("num_experts", ctypes.c_int32),
+        ("topk", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("logits", ctypes.c_int32),
+        ("num_seqs", ctypes.c_int32),
+        ("coef", ctypes.c_float),
+    ]
+
+
 class EPError(RuntimeError):
     def __init__(self, fn: str, code: int, msg: str):
         super().__init__(f"{fn} failed with code {code}: {msg}")
@@ -189,6 +222,21 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     L.ep_lora.restype = ctypes.c_int
     L.ep_lora_backward.argtypes = [P, LS, LW, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, ctypes.c_size_t, vp]
     L.ep_lora_backward.restype = ctypes.c_int
+    LN = ctypes.POINTER(Linear)
+    BL = ctypes.POINTER(Balance)
+    L.ep_expert_linear.argtypes = [P, LS, LN, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+    L.ep_expert_linear.restype = ctypes.c_int
+    L.ep_expert_linear_workspace_bytes.argtypes = [P, LN]
+    L.ep_expert_linear_workspace_bytes.restype = ctypes.c_size_t
+    L.ep_expert_linear_backward.argtypes = [P, LS, LN, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp,
+                                            ctypes.c_size_t, vp]
+    L.ep_expert_linear_backward.restype = ctypes.c_int
+    L.ep_balance_workspace_bytes.argtypes = [BL]
+    L.ep_balance_workspace_bytes.restype = ctypes.c_size_t
+    L.ep_balance_loss.argtypes = [BL, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    L.ep_balance_loss.restype = ctypes.c_int
+    L.ep_balance_loss_backward.argtypes = [BL, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.ep_balance_loss_backward.restype = ctypes.c_int
     L.ep_strerror.argtypes = [ctypes.c_int]
     L.ep_strerror.restype = ctypes.c_char_p
     if path is None:
