@@ -381,9 +381,10 @@ __global__ __launch_bounds__(kThreads) void k_linear(LinearArgs a) {
     constexpr int kWide = kRowAcross ? kBK : kXBK;
     const char* const from = base + st * (kRowAcross ? kBK * a.ldg * 2 : kXBK * 2);
     const bool whole = (st + 1) * kWide <= T.k;
+    auto at = [&](int q) { return from + (KIND == kForward && GATHER ? static_cast<uint64_t>(off[q]) << 4 : off[q]); };
 #pragma unroll
     for (int q = 0; q < kRowLoads; ++q) {
-      const char* p = from + (KIND == kForward && GATHER ? static_cast<uint64_t>(off[q]) << 4 : off[q]);
+      const char* p = at(q);
       if (!whole) {
         const int s = (wave * kRowLoads + q) * 64 + lane;
         const int k = kRowAcross ? s >> 5 : ((s & 7) ^ ((s >> 4) & 7)) * 8;
@@ -417,17 +418,22 @@ __global__ __launch_bounds__(kThreads) void k_linear(LinearArgs a) {
       }
       next_token(st + 1);
     }
+    auto at = [&](int q) {
+      if constexpr (kRowsApart) return from + off[q] + row[q];
+      else return from + (KIND == kForward && q >= 2 ? up_half : 0) + off[q];
+    };
+    if (whole) {
 #pragma unroll
-    for (int q = 0; q < kColLoads; ++q) {
-      const char* p = from + off[q];
-      if constexpr (kRowsApart) p += row[q];
-      if constexpr (KIND == kForward) p += q >= 2 ? up_half : 0;
-      if (!whole) {
-        const int s = ((wave - 4) * kColLoads + q) * 64 + lane;
+      for (int q = 0; q < kColLoads; ++q) load_lds16(at(q), to + q * 1024);
+    } else {
+      int l = lane;
+      asm volatile("" : "+v"(l));
+#pragma unroll
+      for (int q = 0; q < kColLoads; ++q) {
+        const int s = ((wave - 4) * kColLoads + q) * 64 + l;
         const int k = kColAcross ? s >> 5 : ((s & 3) ^ ((s >> 4) & 3)) * 8;
-        if (st * kBK + k >= T.k) p = reinterpret_cast<const char*>(kZeros);
+        load_lds16(st * kBK + k < T.k ? at(q) : reinterpret_cast<const char*>(kZeros), to + q * 1024);
       }
-      load_lds16(p, to + q * 1024);
     }
   };
   // this wave's loads of the stages that step kt reads have landed.  A
@@ -476,6 +482,12 @@ __global__ __launch_bounds__(kThreads) void k_linear(LinearArgs a) {
   // column tile's waves
   float bias_sum = 0.0f;
   const bool want_bias = KIND == kGradW && a.gb != nullptr && T.n0 == 0;
+  int mine[MI];  // i == wn, in terms that the compiler cannot make an index (and scratch memory) of
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    mine[i] = __builtin_amdgcn_readfirstlane(i == wn);
+    if constexpr (KIND == kGradW) asm volatile("" : "+s"(mine[i]));
+  }
 
   // operand addresses within a stage
   const int j16 = lane & 15, g2 = (lane >> 4) & 1;
@@ -514,7 +526,7 @@ __global__ __launch_bounds__(kThreads) void k_linear(LinearArgs a) {
       if (want_bias) {
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-          if (i == wn) {
+          if (mine[i]) {
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
@@ -584,18 +596,21 @@ __global__ __launch_bounds__(kThreads) void k_linear(LinearArgs a) {
     __builtin_amdgcn_wave_barrier();
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   };
-#pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int sub = (2 * i + wm) * 32;
-    if (i >= live) continue;
+#pragma unroll 1  // one copy of the activations' code
+  for (int now = 0; now < live; ++now) {
+    const int sub = (2 * now + wm) * 32;
     settle();
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int i = 0; i < MI; ++i) {
+      if (i != now) continue;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4 v = {acc[i][t][4 * g], acc[i][t][4 * g + 1], acc[i][t][4 * g + 2], acc[i][t][4 * g + 3]};
-        *reinterpret_cast<f32x4*>(slice + lr * kOutPitch + t * 32 + g * 8 + lkv * 4) = v;
-      }
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 v = {acc[i][t][4 * g], acc[i][t][4 * g + 1], acc[i][t][4 * g + 2], acc[i][t][4 * g + 3]};
+          *reinterpret_cast<f32x4*>(slice + lr * kOutPitch + t * 32 + g * 8 + lkv * 4) = v;
+        }
+    }
     settle();
     const int rows = min(32, T.nrows - sub);
     const bool gated = KIND == kForward && a.gated;
