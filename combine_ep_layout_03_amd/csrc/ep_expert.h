@@ -35,6 +35,7 @@ struct LinearArgs {
   uint16_t* gb;  // grad_bias [E, W] or null
   float* part;   // grad_w: fp32 partial sums [splits][E][W][H], then [splits][E][W] of the bias
   int splits;    // parts of each expert's rows (grad_w)
+  int run;       // tiles that an XCD takes in a row
   const int32_t* counts;
   const int32_t* offsets;
   int E, H, N, W;  // W: N, or 2 N if gated
@@ -69,12 +70,12 @@ struct LinearGeom {
   size_t part_bytes;
 };
 LinearGeom linear_geom(int64_t rows, int E, int H, int W);
-// tiles of the largest launch of these sizes
+// tiles of the largest launch of these sizes, at most
 int64_t linear_max_tiles(int64_t rows, int E, int H, int W, int splits);
 
 hipError_t launch_linear(const LinearArgs& a, int64_t rows, hipStream_t s);
 hipError_t launch_linear_grad_x(const LinearArgs& a, int64_t rows, hipStream_t s);
-hipError_t launch_linear_grad_w(const LinearArgs& a, hipStream_t s);
+hipError_t launch_linear_grad_w(const LinearArgs& a, int64_t rows, hipStream_t s);
 hipError_t launch_act_backward(const ActBackwardArgs& a, int64_t rows, hipStream_t s);
 
 // The balance loss.  Tokens are taken in chunks of a fixed size; the part of

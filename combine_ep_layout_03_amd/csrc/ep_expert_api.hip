@@ -35,8 +35,8 @@ int check_linear(const ep_problem_t* p, const ep_linear_t* lin) {
   const int64_t W = lin->gated ? 2LL * lin->n_out : lin->n_out;
   if (p->hidden > kMaxWidth || W > kMaxWidth || W * p->hidden > INT32_MAX) return EP_ENOTSUP;
   const ep::LinearGeom g = ep::linear_geom(max_rows(p), p->num_experts, p->hidden, static_cast<int>(W));
-  // fewer than 2^32 threads in 512 a block
-  if (ep::linear_max_tiles(g.rows, p->num_experts, p->hidden, static_cast<int>(W), g.splits) >= (1 << 23) - 8)
+  // fewer than 2^32 threads in 512 a block, the rounds that a launch is filled up to included
+  if (ep::linear_max_tiles(g.rows, p->num_experts, p->hidden, static_cast<int>(W), g.splits) >= (1 << 22))
     return EP_ENOTSUP;
   return EP_OK;
 }
@@ -155,7 +155,7 @@ int ep_expert_linear_backward(const ep_problem_t* p, const ep_layout_t* L, const
   a.gb = static_cast<uint16_t*>(grad_bias);
   // no row: the weights' gradients are zero, by the same kernel
   if (p->num_tokens == 0)
-    return !grad_w || ep::launch_linear_grad_w(a, stream) == hipSuccess ? EP_OK : EP_EHIP;
+    return !grad_w || ep::launch_linear_grad_w(a, 0, stream) == hipSuccess ? EP_OK : EP_EHIP;
   int64_t ldgo = 0;
   if ((rc = check_stride(grad_out, grad_out_row_stride, a.N, &ldgo)) != EP_OK) return rc;
   if (grad_w && (rc = check_stride(x, x_row_stride, a.H, &a.ldx)) != EP_OK) return rc;
@@ -215,7 +215,7 @@ int ep_expert_linear_backward(const ep_problem_t* p, const ep_layout_t* L, const
   if (grad_w) {
     a.splits = g.splits;
     a.part = static_cast<float*>(workspace);
-    if (ep::launch_linear_grad_w(a, stream) != hipSuccess) return EP_EHIP;
+    if (ep::launch_linear_grad_w(a, g.rows, stream) != hipSuccess) return EP_EHIP;
   }
   return EP_OK;
 }
