@@ -139,9 +139,10 @@ __device__ __forceinline__ void shares(float (&l)[NE], bool sigmoid, float (&res
     const float x = l[i];
     if (sigmoid) {
       const float q = __expf(-fabsf(x));  // exp(-inf) = 0 for an expert that is out
-      const float r = 1.0f / (1.0f + q);
+      const float r = __builtin_amdgcn_rcpf(1.0f + q);
       rest[i] = x >= 0.0f ? q * r : r;
-      l[i] = x >= 0.0f ? r : __expf(x - below) * r;
+      // below = 0 but for tokens of negative logits alone
+      l[i] = x >= 0.0f ? r : (below < 0.0f ? __expf(x - below) : q) * r;
     } else {
       rest[i] = 1.0f;
       l[i] = __expf(x - top);
@@ -159,13 +160,19 @@ __device__ __forceinline__ int64_t offset_of(const BalanceArgs& a, int b) {
   const int64_t v = a.seq[b];
   return v < 0 ? 0 : v > a.T ? a.T : v;
 }
-// the first sequence that ends past token t (B: none)
+// the first sequence that ends past token t (B: none), by 64 probes at a time
 __device__ __forceinline__ int sequence_at(const BalanceArgs& a, int64_t t) {
-  int lo = 0, hi = a.B;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (offset_of(a, mid + 1) > t) hi = mid;
-    else lo = mid + 1;
+  int lo = 0, n = a.B;  // it is one of lo .. lo + n
+  while (n > 0) {
+    const int step = (n + kWave - 1) / kWave;
+    // lane l: does the last of the l-th `step` sequences end past t?
+    const int last = lo + min((lane_id() + 1) * step, n) - 1;
+    const uint64_t past = ballot(lane_id() * step < n && offset_of(a, last + 1) > t);
+    if (past == 0) return lo + n;
+    const int l = __builtin_ctzll(past);
+    lo += l * step;
+    if (step == 1) return lo;
+    n = min(step, n - l * step) - 1;  // the last one is past t
   }
   return lo;
 }
@@ -173,6 +180,7 @@ __device__ __forceinline__ int sequence_at(const BalanceArgs& a, int64_t t) {
 template <int LPT, int NE, int V, typename LT>
 __global__ __launch_bounds__(kBlock) void k_balance(BalanceArgs a, int chunk) {
   constexpr int kPer = kWave / LPT;  // tokens of a wave at once
+  constexpr int kEarly = 2;          // ids a thread: 64 tokens of top-8
   __shared__ float s_sum[kWavesPerBlock][LPT * NE];
   __shared__ int s_count[1024];
   __shared__ int s_tokens;
@@ -181,15 +189,15 @@ __global__ __launch_bounds__(kBlock) void k_balance(BalanceArgs a, int chunk) {
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int g = lane & (LPT - 1);
   const LT* logits = static_cast<const LT*>(a.logits);
-  if (blockIdx.x == 0 && tid == 0) *a.ticket = 0;  // for the join
+  if (blockIdx.x == 0 && tid == 0) *a.total = 0;  // for the join
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * chunk;
   const int64_t t1 = t0 + chunk < a.T ? t0 + chunk : a.T;
   for (int b = sequence_at(a, t0); b < a.B; ++b) {
     const int64_t first = offset_of(a, b);
     if (first >= t1) break;
     const int64_t lo = first > t0 ? first : t0;
-    const int64_t next = offset_of(a, b + 1);
-    const int64_t hi = next < t1 ? next : t1;
+    const int64_t end = offset_of(a, b + 1);
+    const int64_t hi = end < t1 ? end : t1;
     if (hi <= lo) continue;
     for (int e = tid; e < a.E; e += kBlock) s_count[e] = 0;
     if (tid == 0) s_tokens = 0;
@@ -198,10 +206,28 @@ __global__ __launch_bounds__(kBlock) void k_balance(BalanceArgs a, int chunk) {
 #pragma unroll
     for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
     int live = 0;
-    for (int64_t t = lo + wave * kPer + lane / LPT; t < hi; t += kWavesPerBlock * kPer) {
-      if (a.mask && !a.mask[t]) continue;
+    // a row is loaded while the one before is worked on
+    float next[NE];
+    bool next_live = false;
+    auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+      next_live = t < hi && (!a.mask || a.mask[t]);
+      if (t < hi) load_row<LPT, NE, V>(logits + t * a.E, g, a.E, kNegInf, next);
+    };
+    int64_t t = lo + wave * kPer + lane / LPT;
+    fetch(t);
+    // the first ids are on their way meanwhile (T K < 2^31)
+    const uint32_t id_end = static_cast<uint32_t>(hi * a.K);
+    uint32_t at = static_cast<uint32_t>(lo * a.K) + tid;
+    int64_t early[kEarly];
+#pragma unroll
+    for (int j = 0; j < kEarly; ++j) early[j] = at + j * kBlock < id_end ? a.idx[at + j * kBlock] : -1;
+    for (; t < hi; t += kWavesPerBlock * kPer) {
       float l[NE], rest[NE];
-      load_row<LPT, NE, V>(logits + t * a.E, g, a.E, kNegInf, l);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) l[i] = next[i];
+      const bool on = next_live;
+      fetch(t + kWavesPerBlock * kPer);
+      if (!on) continue;
       shares<LPT>(l, a.sigmoid, rest);
 #pragma unroll
       for (int i = 0; i < NE; ++i) acc[i] += l[i];
@@ -220,12 +246,12 @@ __global__ __launch_bounds__(kBlock) void k_balance(BalanceArgs a, int chunk) {
       for (int i = 0; i < NE; ++i) s_sum[wave][element<LPT, NE, V>(g, i)] = acc[i];
     }
     if (live) atomicAdd(&s_tokens, live);
-    // T K < 2^31
-    for (uint32_t i = static_cast<uint32_t>(lo * a.K) + tid; i < static_cast<uint32_t>(hi * a.K); i += kBlock) {
-      if (a.mask && !a.mask[i / static_cast<uint32_t>(a.K)]) continue;
-      const int64_t e = a.idx[i];
-      if (e >= 0 && e < a.E) atomicAdd(&s_count[e], 1);
-    }
+    auto count = [&](uint32_t i, int64_t e) __attribute__((always_inline)) {
+      if (e >= 0 && e < a.E && (!a.mask || a.mask[i / static_cast<uint32_t>(a.K)])) atomicAdd(&s_count[e], 1);
+    };
+#pragma unroll
+    for (int j = 0; j < kEarly; ++j) count(at + j * kBlock, early[j]);
+    for (at += kEarly * kBlock; at < id_end; at += kBlock) count(at, a.idx[at]);
     __syncthreads();
     const int64_t slot = blockIdx.x + static_cast<int64_t>(b);
     for (int e = tid; e < a.E; e += kBlock) {
@@ -240,77 +266,80 @@ __global__ __launch_bounds__(kBlock) void k_balance(BalanceArgs a, int chunk) {
   }
 }
 
-// Block (b, 16 columns): the slots of sequence b added up, 32 runs of slots
-// side by side and then the runs, and the columns' part of the loss; the last
-// block adds the parts.
+// The join's word: how many blocks have added their part of the loss, in the
+// bits above kCountShift, and the sum of the parts as a whole number of
+// 2^-kFraction.  Whole numbers add up to the same in any order, and the block
+// that finds all others counted has the sum in its hand: no other memory has
+// to be ordered between blocks.  (A ticket with fences, each of which writes
+// back an L2, took 18 us for 256 blocks.)  A part is at most E <= 2^10, as is
+// their sum: 2^10 blocks at most leave 53 bits of sum, 42 of them fraction, so
+// the sum is off by 2^10 * 2^-43 at most.
+constexpr int kMaxJoins = 1024;
+constexpr int kCountShift = 53;
+constexpr int kFraction = 42;
+
+// Item (b, 16 columns): the slots of sequence b added up, 32 runs of slots
+// side by side and then the runs, and the columns' part of the loss.
 __global__ __launch_bounds__(kJoinThreads) void k_balance_join(BalanceArgs a, int chunk, int cols) {
   constexpr int kRuns = kJoinThreads / kJoinCols;
   __shared__ float s_sum[kRuns][kJoinCols];
   __shared__ int s_count[kRuns][kJoinCols];
   __shared__ int s_tokens[kRuns];
-  __shared__ double s_loss[kJoinThreads / kWave];
-  __shared__ bool s_last;
   const int tid = threadIdx.x;
   const int run = tid / kJoinCols, c = tid % kJoinCols;
-  const int b = blockIdx.x / cols, group = blockIdx.x % cols;
-  const int e = group * kJoinCols + c;
-  const int64_t first = offset_of(a, b), end = offset_of(a, b + 1);
-  float sum = 0.0f;
-  int count = 0, tokens = 0;
-  if (end > first) {
-    const int64_t s0 = first / chunk + b, s1 = (end - 1) / chunk + b;
-#pragma unroll 4
-    for (int64_t s = s0 + run; s <= s1; s += kRuns) {
-      if (e < a.E) {
-        sum += a.part_sum[s * a.E + e];
-        count += a.part_count[s * a.E + e];
-      }
-      tokens += a.part_tokens[s];
-    }
-  }
-  s_sum[run][c] = sum;
-  s_count[run][c] = count;
-  if (c == 0) s_tokens[run] = tokens;
-  __syncthreads();
   double part = 0.0;
-  if (tid < kJoinCols) {
-    sum = 0.0f;
-    count = tokens = 0;
-    for (int r = 0; r < kRuns; ++r) {
-      sum += s_sum[r][c];
-      count += s_count[r][c];
-      tokens += s_tokens[r];
+  for (int item = blockIdx.x; item < a.B * cols; item += gridDim.x) {
+    const int b = item / cols;
+    const int e = item % cols * kJoinCols + c;
+    const int64_t first = offset_of(a, b), end = offset_of(a, b + 1);
+    float sum = 0.0f;
+    int count = 0, tokens = 0;
+    if (end > first) {
+      const int64_t s0 = first / chunk + b, s1 = (end - 1) / chunk + b;
+#pragma unroll 4
+      for (int64_t s = s0 + run; s <= s1; s += kRuns) {
+        if (e < a.E) {
+          sum += a.part_sum[s * a.E + e];
+          count += a.part_count[s * a.E + e];
+        }
+        tokens += a.part_tokens[s];
+      }
     }
-    if (e < a.E) {
-      const float mean = tokens > 0 ? sum / static_cast<float>(tokens) : 0.0f;
-      a.mean[static_cast<int64_t>(b) * a.E + e] = mean;
-      a.counts[static_cast<int64_t>(b) * a.E + e] = count;
-      if (tokens > 0) part = static_cast<double>(count) * mean / tokens;
+    s_sum[run][c] = sum;
+    s_count[run][c] = count;
+    if (c == 0) s_tokens[run] = tokens;
+    __syncthreads();
+    if (tid < kJoinCols) {
+      sum = 0.0f;
+      count = tokens = 0;
+#pragma unroll 8
+      for (int r = 0; r < kRuns; ++r) {
+        sum += s_sum[r][c];
+        count += s_count[r][c];
+        tokens += s_tokens[r];
+      }
+      if (e < a.E) {
+        const float mean = tokens > 0 ? sum / static_cast<float>(tokens) : 0.0f;
+        a.mean[static_cast<int64_t>(b) * a.E + e] = mean;
+        a.counts[static_cast<int64_t>(b) * a.E + e] = count;
+        if (tokens > 0) part += static_cast<double>(count) * mean / tokens;
+      }
+      if (e == 0) a.tokens[b] = tokens;
     }
-    if (e == 0) a.tokens[b] = tokens;
-#pragma unroll
-    for (int off = 1; off < kJoinCols; off <<= 1) part += __shfl_xor(part, off, kJoinCols);
-    if (tid == 0) {
-      a.part_loss[blockIdx.x] = part;
-      __threadfence();
-      s_last = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
-    }
+    __syncthreads();
   }
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  double total = 0.0;
-  for (int64_t i = tid; i < static_cast<int64_t>(gridDim.x); i += kJoinThreads)
-    total += __hip_atomic_load(a.part_loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (tid >= kJoinCols) return;
 #pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) total += __shfl_xor(total, off, kWave);
-  if ((tid & (kWave - 1)) == 0) s_loss[tid / kWave] = total;
-  __syncthreads();
-  if (tid == 0) {
-    total = 0.0;
-    for (int w = 0; w < kJoinThreads / kWave; ++w) total += s_loss[w];
-    a.loss[0] = static_cast<float>(total * a.scale);
-  }
+  for (int off = 1; off < kJoinCols; off <<= 1) part += __shfl_xor(part, off, kJoinCols);
+  if (tid != 0) return;
+  // offsets out of order may give anything
+  part = fmin(fmax(part * a.E / (static_cast<double>(a.K) * a.B), 0.0), static_cast<double>(a.E));
+  const unsigned long long mine =
+      static_cast<unsigned long long>(part * (1ull << kFraction) + 0.5) + (1ull << kCountShift);
+  const unsigned long long before = __hip_atomic_fetch_add(a.total, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if ((before >> kCountShift) != gridDim.x - 1) return;
+  const unsigned long long all = (before + mine) & ((1ull << kCountShift) - 1);
+  a.loss[0] = static_cast<float>(static_cast<double>(all) / (1ull << kFraction) * a.coef);
 }
 
 // no token: every output is 0
@@ -434,7 +463,8 @@ BalanceGeom balance_geom(int64_t T, int E, int B) {
   g.sum_bytes = up(static_cast<size_t>(g.slots) * E * 4);
   g.count_bytes = up(static_cast<size_t>(g.slots) * E * 4);
   g.token_bytes = up(static_cast<size_t>(g.slots) * 4);
-  g.loss_bytes = up(static_cast<size_t>(B) * g.cols * 8);
+  const int64_t items = static_cast<int64_t>(B) * g.cols;
+  g.joins = static_cast<int>(items < kMaxJoins ? items : kMaxJoins);
   return g;
 }
 
@@ -450,7 +480,7 @@ hipError_t launch_balance(const BalanceArgs& a, const BalanceGeom& g, hipStream_
 #undef EP_LAUNCH
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  k_balance_join<<<static_cast<unsigned>(a.B * g.cols), kJoinThreads, 0, s>>>(a, g.chunk, g.cols);
+  k_balance_join<<<static_cast<unsigned>(g.joins), kJoinThreads, 0, s>>>(a, g.chunk, g.cols);
   return hipGetLastError();
 }
 

@@ -86,9 +86,10 @@ struct BalanceGeom {
   int64_t chunks;  // ceil(T / chunk)
   int64_t slots;   // chunks + B
   int cols;        // column groups of the join, ceil(E / 16)
-  // workspace parts, multiples of 16
-  size_t sum_bytes, count_bytes, token_bytes, loss_bytes;
-  size_t bytes() const { return sum_bytes + count_bytes + token_bytes + loss_bytes + 16; }
+  int joins;       // blocks of the join
+  // workspace parts, multiples of 16, and the word that the join's blocks add to
+  size_t sum_bytes, count_bytes, token_bytes;
+  size_t bytes() const { return sum_bytes + count_bytes + token_bytes + 16; }
 };
 BalanceGeom balance_geom(int64_t T, int E, int B);
 
@@ -108,13 +109,13 @@ struct BalanceArgs {
   int E, K, B;
   bool sigmoid, bf16;
   float scale;  // coef * E / (K * B)
-  // workspace: by slot, sums [slots, E], counts [slots, E], tokens [slots];
-  // losses of (sequence, column group); the ticket of the join's blocks
+  float coef;
+  // workspace: by slot, sums [slots, E], counts [slots, E], tokens [slots]; the
+  // join's word
   float* part_sum;
   int32_t* part_count;
   int32_t* part_tokens;
-  double* part_loss;
-  uint32_t* ticket;
+  unsigned long long* total;
 };
 hipError_t launch_balance(const BalanceArgs& a, const BalanceGeom& g, hipStream_t s);
 hipError_t launch_balance_backward(const BalanceArgs& a, hipStream_t s);

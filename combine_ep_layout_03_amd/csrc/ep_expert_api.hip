@@ -92,6 +92,7 @@ ep::BalanceArgs balance_args(const ep_balance_t* b) {
   a.B = b->num_seqs;
   a.sigmoid = b->score == EP_SCORE_SIGMOID;
   a.bf16 = b->logits == EP_LOGITS_BF16;
+  a.coef = b->coef;
   a.scale = static_cast<float>(static_cast<double>(b->coef) * b->num_experts /
                                (static_cast<double>(b->topk) * b->num_seqs));
   return a;
@@ -268,8 +269,7 @@ int ep_balance_loss(const ep_balance_t* b, const void* logits, const int64_t* to
     a.part_sum = reinterpret_cast<float*>(part(g.sum_bytes));
     a.part_count = reinterpret_cast<int32_t*>(part(g.count_bytes));
     a.part_tokens = reinterpret_cast<int32_t*>(part(g.token_bytes));
-    a.part_loss = reinterpret_cast<double*>(part(g.loss_bytes));
-    a.ticket = reinterpret_cast<uint32_t*>(ws);
+    a.total = reinterpret_cast<unsigned long long*>(ws);
   }
   return ep::launch_balance(a, g, stream) == hipSuccess ? EP_OK : EP_EHIP;
 }

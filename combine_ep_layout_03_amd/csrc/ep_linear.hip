@@ -109,27 +109,28 @@ __device__ __forceinline__ float normal_cdf(float z) {
   return z < 0.0f ? tail : 1.0f - tail;
 }
 
-// 8 values become their activations
+// N values become their activations
+template <int N>
 __device__ __forceinline__ void act_values(float* z, int act) {
   switch (act) {
     case kActRelu:
 #pragma unroll
-      for (int d = 0; d < 8; ++d) z[d] = z[d] < 0.0f ? 0.0f : z[d];
+      for (int d = 0; d < N; ++d) z[d] = z[d] < 0.0f ? 0.0f : z[d];
       break;
     case kActSilu:
 #pragma unroll
-      for (int d = 0; d < 8; ++d) z[d] *= sigmoid(z[d]);
+      for (int d = 0; d < N; ++d) z[d] *= sigmoid(z[d]);
       break;
     case kActGelu:
 #pragma unroll
-      for (int d = 0; d < 8; ++d) {
+      for (int d = 0; d < N; ++d) {
         z[d] *= normal_cdf(z[d]);
         if (d & 1) __builtin_amdgcn_sched_barrier(0);  // two at a time, for want of registers
       }
       break;
     case kActGeluTanh:
 #pragma unroll
-      for (int d = 0; d < 8; ++d) z[d] *= sigmoid(2.0f * kTanhScale * (z[d] + kTanhCubic * z[d] * z[d] * z[d]));
+      for (int d = 0; d < N; ++d) z[d] *= sigmoid(2.0f * kTanhScale * (z[d] + kTanhCubic * z[d] * z[d] * z[d]));
       break;
     default:
       break;
@@ -620,7 +621,7 @@ __global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(Linea
 #pragma unroll
         for (int d = 0; d < 32; d += 8) {
           if (gated && d >= 16) break;
-          act_values(z + d, a.act);
+          act_values<8>(z + d, a.act);
         }
         if (gated) {
 #pragma unroll
@@ -709,6 +710,149 @@ __global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(Linea
   }
   // nobody reads the ring any more: every wave passed the last step's barrier
   finish();
+}
+
+// ---------------------------------------------------------------- few rows
+// Forward where experts have a few rows each (a decoding step: the weights are
+// read once and nothing else counts), or the whole problem is small.  A block
+// takes 64 of an expert's columns (32 gate and 32 up with a gate) and 16 of
+// its rows; its 8 waves take the 128-byte lines of the contraction in turn.  Weights and rows go
+// straight from memory into the operands of v_mfma_f32_16x16x32_bf16 (a
+// load instruction takes 64 bytes of 16 weight rows), a line ahead of the
+// product, so a wave keeps 8 KiB of weights in flight and waits for nobody;
+// the waves' sums meet in LDS at the end, in their order.  16 tokens x 4096 ->
+// 2 x 2048, top-4 of 64 experts: 244 us, 5.6 TB/s of weights (the tiles above:
+// 260; two lines ahead 250, non-temporal weights 246, 32 rows a block 254); one
+// expert of 16 rows, 4096 -> 4096: 21 us (56).
+template <bool GATHER>
+__global__ __launch_bounds__(kThreads, 4) void k_linear_few(LinearArgs a) {
+  constexpr int kWaves = kThreads / kWave;
+  constexpr int kRows = 16;
+  __shared__ __align__(16) f32x4 s_sum[kWaves][4][kWave];
+  static_assert((1024 + kWaves) * 4 <= sizeof(s_sum), "tile table fits");
+  int* const sTiles = reinterpret_cast<int*>(s_sum);
+  if (!layout_current(a.status, a.generation)) return;
+  const int tid = threadIdx.x;
+  const int lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int tile_cols = a.gated ? 32 : 64;
+  const int nt = (a.N + tile_cols - 1) / tile_cols;
+
+  for (int e = tid; e < a.E; e += kThreads) sTiles[e] = (a.counts[e] + kRows - 1) / kRows * nt;
+  __syncthreads();
+  const int total = __builtin_amdgcn_readfirstlane(block_exclusive_scan<kThreads>(sTiles, a.E, sTiles + 1024));
+  if (total == 0) return;
+  const int tile = tile_at(static_cast<int>(blockIdx.x / kXcds), total, a.run);
+  if (tile >= total) return;
+  int lo = 0, hi = a.E - 1;  // the last expert whose first tile is not past it
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__builtin_amdgcn_readfirstlane(sTiles[mid]) <= tile) lo = mid;
+    else hi = mid - 1;
+  }
+  const int e = lo;
+  const int cnt = a.counts[e];
+  const int mt = (cnt + kRows - 1) / kRows;
+  const int local = tile - __builtin_amdgcn_readfirstlane(sTiles[e]);
+  // row tiles of the same columns side by side: they share weights
+  const int im = local % mt;
+  const int n0 = local / mt * tile_cols;
+  const int per = (cnt + mt - 1) / mt;
+  const int64_t row0 = a.offsets[e] + im * per;
+  const int nrows = min(per, cnt - im * per);
+  __syncthreads();  // the table is read before the sums are written
+
+  const int m = lane & 15, q = lane >> 4;
+  const uint16_t* wp[4];
+#pragma unroll
+  for (int f = 0; f < 4; ++f) {
+    const int c = n0 + (a.gated ? f & 1 : f) * 16 + m;
+    const int64_t w = (c < a.N ? c : n0) + (a.gated && f >= 2 ? a.N : 0);
+    wp[f] = a.w + (static_cast<int64_t>(e) * a.W + w) * a.H + q * 8;
+  }
+  const int64_t xr = row0 + (m < nrows ? m : 0);
+  const uint16_t* const xp = a.x + (GATHER ? static_cast<int64_t>(a.xmap[xr]) : xr) * a.ldx + q * 8;
+  f32x4 acc[4];
+#pragma unroll
+  for (int f = 0; f < 4; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  struct Line {
+    bf16x8 w[2][4], x[2];
+  };
+  auto load = [&](int line, Line& l) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = line * 64 + h * 32;
+#pragma unroll
+      for (int f = 0; f < 4; ++f) l.w[h][f] = *reinterpret_cast<const bf16x8*>(wp[f] + k);
+      l.x[h] = *reinterpret_cast<const bf16x8*>(xp + k);
+    }
+  };
+  auto multiply = [&](const Line& l) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(l.w[h][f], l.x[h], acc[f], 0, 0, 0);
+  };
+  const int lines = a.H / 64;  // whole ones
+  Line one, two;
+  int at = wave;
+  if (at < lines) load(at, one);
+  while (at < lines) {
+    if (at + kWaves < lines) load(at + kWaves, two);
+    multiply(one);
+    at += kWaves;
+    if (at >= lines) break;
+    if (at + kWaves < lines) load(at + kWaves, one);
+    multiply(two);
+    at += kWaves;
+  }
+  if (at == lines && a.H % 64) {  // the rest, by the wave whose turn it is; zeros past its end
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = lines * 64 + h * 32;
+      const bool in = k + q * 8 < a.H;
+#pragma unroll
+      for (int f = 0; f < 4; ++f) one.w[h][f] = in ? *reinterpret_cast<const bf16x8*>(wp[f] + k) : bf16x8{};
+      one.x[h] = in ? *reinterpret_cast<const bf16x8*>(xp + k) : bf16x8{};
+    }
+    multiply(one);
+  }
+#pragma unroll
+  for (int f = 0; f < 4; ++f) s_sum[wave][f][lane] = acc[f];
+  __syncthreads();
+
+  // lane l of a sum holds row l % 16 and columns (l / 16) * 4 .. + 3
+  const int f = wave, r = m, n = n0 + f * 16 + q * 4;
+  if (f < (a.gated ? 2 : 4) && r < nrows && n < a.N) {
+    f32x4 v = s_sum[0][f][lane];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v += s_sum[w][f][lane];
+    const int64_t row = row0 + r;
+    auto load4 = [&](const uint16_t* p) __attribute__((always_inline)) {
+      const u32x2 b = *reinterpret_cast<const u32x2*>(p);
+      return f32x4{bf16_lo(b[0]), bf16_hi(b[0]), bf16_lo(b[1]), bf16_hi(b[1])};
+    };
+    auto store4 = [&](uint16_t* p, const f32x4& x) __attribute__((always_inline)) {
+      *reinterpret_cast<u32x2*>(p) = u32x2{bf16x2_of(x[0], x[1]), bf16x2_of(x[2], x[3])};
+    };
+    const uint16_t* bias = a.bias ? a.bias + static_cast<int64_t>(e) * a.W : nullptr;
+    if (bias) v += load4(bias + n);
+    if (a.pre) store4(a.pre + row * a.ldpre + n, v);
+    float z[4] = {v[0], v[1], v[2], v[3]};
+    act_values<4>(z, a.act);
+    v = f32x4{z[0], z[1], z[2], z[3]};
+    if (a.gated) {
+      f32x4 u = s_sum[0][2 + f][lane];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) u += s_sum[w][2 + f][lane];
+      if (bias) u += load4(bias + a.N + n);
+      if (a.pre) store4(a.pre + row * a.ldpre + a.N + n, u);
+      v *= u;
+    }
+    if (a.res) v += load4(a.res + row * a.ldres + n);
+    store4(a.out + row * a.ldout + n, v);
+  }
 }
 
 // Weight gradients of split rows: the parts' sum, in their order.  8 elements
@@ -809,7 +953,9 @@ hipError_t launch_rows(const LinearArgs& a, int64_t rows, int64_t nt, hipStream_
     const double per = static_cast<double>(ceil_div(ceil_div(static_cast<int64_t>(ceil(most)), mt), 32) * 32);
     // two blocks of 128 rows share a CU
     const int64_t places = kXcds * kCusPerXcd * (mi == 2 ? 2 : 1);
-    const double cost = static_cast<double>(ceil_div(mt * a.E * nt, places) * (mi == 2 ? 2 : 1)) * (per + 64.0);
+    const int64_t tiles = mt * a.E * nt;
+    const int64_t turns = ceil_div(tiles, places) * (mi == 2 && tiles > places / 2 ? 2 : 1);
+    const double cost = static_cast<double>(turns) * (per + 64.0);
     if (best == 0 || cost < least) {
       best = mi;
       least = cost;
@@ -848,10 +994,24 @@ int64_t linear_max_tiles(int64_t rows, int E, int H, int W, int splits) {
   // columns of 128 (gated) or 256, rows of 128 at least
   const int64_t by_rows = row_tiles(rows, E, 128) * ceil_div(W > H ? W : H, 128);
   const int64_t by_weights = ceil_div(W, 128) * ceil_div(H, kBN) * E * splits;
-  return by_rows > by_weights ? by_rows : by_weights;
+  const int64_t few = rows <= 4 * static_cast<int64_t>(E) ? row_tiles(rows, E, 16) * ceil_div(W, 64) : 0;
+  const int64_t tiles = by_rows > by_weights ? by_rows : by_weights;
+  return few > tiles ? few : tiles;
 }
 
 hipError_t launch_linear(const LinearArgs& a, int64_t rows, hipStream_t s) {
+  // Up to 4 rows an expert, or few enough 16 x 64 pieces that the tiles of
+  // 128 rows and more would leave most CUs idle (8 experts of 127 rows, 1032 ->
+  // 520: 13.5 us against 24; 64 of 16 rows, 4096 -> 2 x 2048: 432 against 381)
+  const int64_t few_nt = ceil_div(a.N, a.gated ? 32 : 64);
+  if (rows <= 4 * static_cast<int64_t>(a.E) || ceil_div(ceil_div(rows, a.E), 16) * a.E * few_nt <= 1024) {
+    LinearArgs b = a;
+    b.run = INT_MAX;
+    const unsigned blocks = blocks_of(row_tiles(rows, a.E, 16) * few_nt, b.run);
+    if (a.xmap) k_linear_few<true><<<blocks, kThreads, 0, s>>>(b);
+    else k_linear_few<false><<<blocks, kThreads, 0, s>>>(b);
+    return hipGetLastError();
+  }
   const int64_t nt = ceil_div(a.N, a.gated ? kBN / 2 : kBN);
   return a.xmap ? launch_rows<kForward, true>(a, rows, nt, s) : launch_rows<kForward, false>(a, rows, nt, s);
 }
