@@ -50,6 +50,14 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
       reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p));
 }
 
+// a pointer that is the same in every lane, as the compiler may not know
+__device__ __forceinline__ const char* scalar(const char* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<int>(v >> 32));
+  return reinterpret_cast<const char*>((static_cast<uint64_t>(hi) << 32) | lo);
+}
+
 // 16 bytes a lane from base + off to LDS at `to` + 16 lane, not tracked by the
 // compiler: its wait counts cannot tell the stages of a ring apart, and would
 // drain every load before each LDS read.  wait_vm below is what waits.
@@ -243,7 +251,6 @@ __global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(Linea
   char* const sCol = lds + kRowStages * kRowBytes;
   int* const sTiles = reinterpret_cast<int*>(lds);
 
-  if (!layout_current(a.status, a.generation)) return;
   const int tid = threadIdx.x;
   const int lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -257,36 +264,41 @@ __global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(Linea
   const int nt = (cols + tile_cols - 1) / tile_cols;
 
   // ---- tiles
-  int total;  // tiles, below 2^22
+  Tile T;
+  int im, jn;
   if constexpr (KIND == kGradW) {
-    total = a.E * a.splits * ((a.W + kBM - 1) / kBM) * nt;
+    const int mt = (a.W + kBM - 1) / kBM;
+    const int total = a.E * a.splits * mt * nt;  // below 2^22
+    const int tile = tile_at(static_cast<int>(blockIdx.x / kXcds), total, a.run);
+    if (tile >= total) return;
+    const int es = tile / (mt * nt);
+    T.e = es / a.splits;
+    // three words from memory, together: short contractions feel each latency
+    int32_t stamp = a.status[kStatusGeneration];
+    int cnt = a.counts[T.e], offset = a.offsets[T.e];
+    asm volatile("" : "+s"(stamp), "+s"(cnt), "+s"(offset));
+    cnt = __builtin_amdgcn_readfirstlane(cnt);
+    offset = __builtin_amdgcn_readfirstlane(offset);
+    if (!layout_current(a.status, stamp, a.generation)) return;
+    tile_of(tile - es * mt * nt, mt, nt, im, jn);
+    T.split = es - T.e * a.splits;
+    const int per = ((cnt + a.splits - 1) / a.splits + kBK - 1) / kBK * kBK;
+    const int first = min(cnt, per * T.split);
+    T.row0 = offset + first;
+    T.k = min(per, cnt - first);
+    T.r0 = im * kBM;
+    T.nrows = min(kBM, a.W - T.r0);
   } else {
+    if (!layout_current(a.status, a.generation)) return;
     // row tiles of each expert times column tiles, then their exclusive
     // prefix (the same in every block)
     for (int e = tid; e < a.E; e += kThreads) sTiles[e] = (a.counts[e] + kBM - 1) / kBM * nt;
     __syncthreads();
     // values from LDS are the same in every lane: scalar from here on
-    total = __builtin_amdgcn_readfirstlane(block_exclusive_scan<kThreads>(sTiles, a.E, sTiles + 1024));
-  }
-  if (total == 0) return;
-  const int tile = tile_at(static_cast<int>(blockIdx.x / kXcds), total, a.run);
-  if (tile >= total) return;
-  Tile T;
-  int im, jn;
-  if constexpr (KIND == kGradW) {
-    const int mt = (a.W + kBM - 1) / kBM;
-    const int es = tile / (mt * nt);
-    tile_of(tile - es * mt * nt, mt, nt, im, jn);
-    T.e = es / a.splits;
-    T.split = es - T.e * a.splits;
-    const int cnt = a.counts[T.e];
-    const int per = ((cnt + a.splits - 1) / a.splits + kBK - 1) / kBK * kBK;
-    const int first = min(cnt, per * T.split);
-    T.row0 = a.offsets[T.e] + first;
-    T.k = min(per, cnt - first);
-    T.r0 = im * kBM;
-    T.nrows = min(kBM, a.W - T.r0);
-  } else {
+    const int total = __builtin_amdgcn_readfirstlane(block_exclusive_scan<kThreads>(sTiles, a.E, sTiles + 1024));
+    if (total == 0) return;
+    const int tile = tile_at(static_cast<int>(blockIdx.x / kXcds), total, a.run);
+    if (tile >= total) return;
     // the last expert whose first tile is not past it (empty ones repeat the
     // prefix of the next)
     int lo = 0, hi = a.E - 1;
@@ -296,12 +308,12 @@ __global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(Linea
       else hi = mid - 1;
     }
     T.e = lo;
-    const int cnt = a.counts[lo];
+    const int cnt = __builtin_amdgcn_readfirstlane(a.counts[lo]);
     const int mt = (cnt + kBM - 1) / kBM;
     tile_of(tile - __builtin_amdgcn_readfirstlane(sTiles[lo]), mt, nt, im, jn);
     // the rows split evenly over the tiles, in steps of 32: none is empty
     const int per = ((cnt + mt - 1) / mt + 31) / 32 * 32;
-    T.row0 = a.offsets[lo] + im * per;
+    T.row0 = __builtin_amdgcn_readfirstlane(a.offsets[lo]) + im * per;
     T.nrows = min(per, cnt - im * per);
     T.k = KIND == kForward ? a.H : a.W;
     T.r0 = T.split = 0;
@@ -369,7 +381,7 @@ __global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(Linea
       if constexpr (KIND == kGradW) from = GATHER ? a.x : a.x + T.row0 * a.ldx;
       else from = a.w + (static_cast<int64_t>(T.e) * a.W + (KIND == kForward ? T.n0 : 0)) * a.H;
     }
-    base = reinterpret_cast<const char*>(from);
+    base = scalar(reinterpret_cast<const char*>(from));
   };
   auto issue_row = [&](int st) __attribute__((always_inline)) {
     const uint32_t to = lds_addr(sRow) + (st % kRowStages) * kRowBytes + wave * kRowLoads * 1024;
@@ -562,6 +574,44 @@ __global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(Linea
         }
       }
     }
+    if constexpr (KIND != kForward) {
+      if (KIND == kGradX || a.splits == 1) {
+        // no arithmetic is left: up to four sub-tiles at once, each through a slice of its own
+        uint16_t* const to = KIND == kGradX ? a.out + T.row0 * a.ldout
+                                            : a.gw + (static_cast<int64_t>(T.e) * a.W + T.r0) * a.H;
+        const int64_t ld = KIND == kGradX ? a.ldout : a.H;
+        constexpr int kAtOnce = MI == 5 ? 4 : MI;
+        static_assert(kAtOnce * 8 * 4096 <= kRing, "slices fit");
+#pragma unroll
+        for (int i0 = 0; i0 < MI; i0 += kAtOnce) {
+          settle();
+#pragma unroll
+          for (int i = i0; i < MI && i < i0 + kAtOnce; ++i) {
+            if (i >= live) continue;
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              const f32x16& v = acc[i][g >> 2];
+              const int d = (g & 3) * 4;
+              *reinterpret_cast<Lds8>(piece(lr, g) + (i - i0) * 8 * 4096 + lkv * 8) =
+                  u32x2{bf16x2_of(v[d], v[d + 1]), bf16x2_of(v[d + 2], v[d + 3])};
+            }
+          }
+          settle();
+#pragma unroll
+          for (int i = i0; i < MI && i < i0 + kAtOnce; ++i) {
+            if (i >= live) continue;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int r = j * 8 + (lane >> 3), c = lane & 7;
+              const int row = (2 * i + wm) * 32 + r, n = col0 + c * 8;
+              if (row < T.nrows && n < a.H)
+                *reinterpret_cast<u32x4*>(to + row * ld + n) = *reinterpret_cast<Lds16>(piece(r, c) + (i - i0) * 8 * 4096);
+            }
+          }
+        }
+        return;
+      }
+    }
 #pragma unroll 1  // one copy of the code
     for (int now = 0; now < live; ++now) {
       int l = lane;  // opaque: no address is formed ahead of the loop and kept through it
@@ -587,7 +637,7 @@ __global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(Linea
         }
         settle();
         const int shift = pieces == 8 ? 3 : 2;
-        #pragma unroll 1
+#pragma unroll 1
         for (int it = l; it < rows << shift; it += kWave) {
           const int r = it >> shift, c = it & (pieces - 1);
           uint16_t* const at = to(r, c);
@@ -640,20 +690,10 @@ __global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(Linea
           const int n = col0 + c * 8;
           return n < a.N ? a.out + (row + r) * a.ldout + n : nullptr;
         });
-      } else if constexpr (KIND == kGradX) {
-        emit(8, [&](int r, int c) {
-          const int n = col0 + c * 8;
-          return n < a.H ? a.out + (T.row0 + sub + r) * a.ldout + n : nullptr;
-        });
-      } else {
-        const int64_t first = (static_cast<int64_t>(T.e) * a.W + T.r0 + sub) * a.H;
-        if (a.splits == 1) {
-          emit(8, [&](int r, int c) {
-            const int n = col0 + c * 8;
-            return n < a.H ? a.gw + first + static_cast<int64_t>(r) * a.H + n : nullptr;
-          });
-        } else if (er < rows) {
-          float* const to = a.part + static_cast<int64_t>(T.split) * a.E * a.W * a.H + first + static_cast<int64_t>(er) * a.H;
+      } else if constexpr (KIND == kGradW) {  // a part of split rows
+        if (er < rows) {
+          float* const to =
+              a.part + ((static_cast<int64_t>(T.split) * a.E + T.e) * a.W + T.r0 + sub + er) * static_cast<int64_t>(a.H);
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
             const int n = col0 + g * 8 + eh * 4;
@@ -1021,11 +1061,11 @@ hipError_t launch_linear_grad_x(const LinearArgs& a, int64_t rows, hipStream_t s
 }
 
 hipError_t launch_linear_grad_w(const LinearArgs& a, int64_t rows, hipStream_t s) {
-  // Where experts have up to 32 rows, writing the result is all: 128 x 256
-  // tiles, two blocks a CU (64 experts of 4 rows, 2.1 GB of gradients: 342 us
-  // against 407; of 64 rows 583 both).
+  // Where experts have few rows, starting a tile and writing it take the time:
+  // 128 x 256 tiles, two blocks a CU (64 experts of 4 rows, 2.1 GB of gradients:
+  // 358 us, 256 x 256 tiles 460; of 64 rows 500 and 594; of 256 rows 985 and 948).
   const int64_t avg = rows / a.E;
-  const bool half = avg <= 32;
+  const bool half = avg <= 128;
   const int64_t per_expert = ceil_div(a.W, half ? 128 : 256) * ceil_div(a.H, kBN) * a.splits;
   const int64_t tiles = per_expert * a.E;
   // Runs of 32 tiles spread experts of many rows over the XCDs.  Where an
