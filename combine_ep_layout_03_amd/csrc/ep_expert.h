@@ -33,9 +33,10 @@ struct LinearArgs {
   int64_t ldpre;
   uint16_t* gw;  // grad_w [E, W, H]
   uint16_t* gb;  // grad_bias [E, W] or null
-  float* part;   // grad_w: fp32 partial sums [splits][E][W][H], then [splits][E][W] of the bias
+  float* part;   // grad_w: workspace, fp32 partial sums [splits][E][W][H], then [splits][E][W] of the bias
   int splits;    // parts of each expert's rows (grad_w)
   int run;       // tiles that an XCD takes in a row
+  int32_t* even;  // grad_w: 0 there: runs of 32 instead; null: as run says
   const int32_t* counts;
   const int32_t* offsets;
   int E, H, N, W;  // W: N, or 2 N if gated
@@ -67,7 +68,7 @@ struct ActBackwardArgs {
 struct LinearGeom {
   int64_t rows;  // expert-major rows at most, padding included
   int splits;    // parts of each expert's rows in the weight gradient
-  size_t part_bytes;
+  size_t part_bytes;  // of workspace, 16 at least
 };
 LinearGeom linear_geom(int64_t rows, int E, int H, int W);
 // tiles of the largest launch of these sizes, at most

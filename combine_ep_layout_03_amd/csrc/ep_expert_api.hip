@@ -135,8 +135,7 @@ int ep_expert_linear(const ep_problem_t* p, const ep_layout_t* L, const ep_linea
 
 size_t ep_expert_linear_workspace_bytes(const ep_problem_t* p, const ep_linear_t* lin) {
   if (check_linear(p, lin) != EP_OK) return 0;
-  const size_t n = ep::linear_geom(max_rows(p), p->num_experts, p->hidden, width_of(lin)).part_bytes;
-  return n > 0 ? n : 16;  // 0 means refused
+  return ep::linear_geom(max_rows(p), p->num_experts, p->hidden, width_of(lin)).part_bytes;
 }
 
 int ep_expert_linear_backward(const ep_problem_t* p, const ep_layout_t* L, const ep_linear_t* lin,
@@ -185,7 +184,7 @@ int ep_expert_linear_backward(const ep_problem_t* p, const ep_layout_t* L, const
   if (!(pre == grad_pre && b.ldpre == b.ldgpre) && any_overlap(gp, {rp})) return EP_EINVAL;
   if (!workspace || !aligned(workspace, 16)) return EP_EINVAL;
   if (workspace_bytes < g.part_bytes) return EP_EWORKSPACE;
-  if (g.part_bytes > 0 && workspace_overlaps(workspace, g.part_bytes, {ro, rx, rw, rp, gp, gx, gw, gb})) return EP_EINVAL;
+  if (workspace_overlaps(workspace, g.part_bytes, {ro, rx, rw, rp, gp, gx, gw, gb})) return EP_EINVAL;
   a.x = static_cast<const uint16_t*>(x);
   if (bare) {
     a.g = static_cast<const uint16_t*>(grad_out);

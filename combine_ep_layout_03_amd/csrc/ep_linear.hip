@@ -287,7 +287,8 @@ __global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(Linea
   if constexpr (KIND == kGradW) {
     const int mt = (a.W + kBM - 1) / kBM;
     const int total = a.E * a.splits * mt * nt;  // below 2^22
-    const int tile = tile_at(static_cast<int>(blockIdx.x / kXcds), total, a.run);
+    const int run = a.even && *a.even == 0 ? kCusPerXcd : a.run;
+    const int tile = tile_at(static_cast<int>(blockIdx.x / kXcds), total, run);
     if (tile >= total) return;
     const int es = tile / (mt * nt);
     T.e = es / a.splits;
@@ -913,6 +914,34 @@ __global__ __launch_bounds__(kThreads, 4) void k_linear_few(LinearArgs a) {
   }
 }
 
+// Do the experts have much the same rows (none over 3/2 of the mean)?
+__global__ __launch_bounds__(kBlock) void k_linear_even(const int32_t* counts, int E, int32_t* even, int32_t* status,
+                                                        uint32_t generation) {
+  __shared__ int s_most[kWavesPerBlock], s_all[kWavesPerBlock];
+  if (!layout_current(status, generation)) return;
+  int most = 0, all = 0;
+  for (int e = threadIdx.x; e < E; e += kBlock) {
+    most = max(most, counts[e]);
+    all += counts[e];
+  }
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) {
+    most = max(most, __shfl_xor(most, off, kWave));
+    all += __shfl_xor(all, off, kWave);
+  }
+  if ((threadIdx.x & (kWave - 1)) == 0) {
+    s_most[threadIdx.x / kWave] = most;
+    s_all[threadIdx.x / kWave] = all;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < kWavesPerBlock; ++w) {
+    most = max(most, s_most[w]);
+    all += s_all[w];
+  }
+  *even = 2ll * most * E <= 3ll * all;
+}
+
 // Weight gradients of split rows: the parts' sum, in their order.  8 elements
 // a thread; the bias's parts follow the weights'.
 __global__ __launch_bounds__(kBlock) void k_linear_join(const float* part, int splits, int64_t nw, int64_t nb,
@@ -1044,7 +1073,7 @@ LinearGeom linear_geom(int64_t rows, int E, int H, int W) {
   const int64_t most = rows / E / 256;
   if (splits > most) splits = most;
   g.splits = static_cast<int>(splits > 1 ? splits : 1);
-  g.part_bytes = g.splits > 1 ? (static_cast<size_t>(W) * H + W) * E * g.splits * 4 : 0;
+  g.part_bytes = g.splits > 1 ? (static_cast<size_t>(W) * H + W) * E * g.splits * 4 : 16;
   return g;
 }
 
@@ -1086,13 +1115,24 @@ hipError_t launch_linear_grad_w(const LinearArgs& a, int64_t rows, hipStream_t s
   const bool half = avg <= 128;
   const int64_t per_expert = ceil_div(a.W, half ? 128 : 256) * ceil_div(a.H, kBN) * a.splits;
   const int64_t tiles = per_expert * a.E;
-  // Runs of 32 tiles spread experts of many rows over the XCDs.  Where an
-  // expert's rows fit an L2 (4 MiB) and there are many experts, an XCD takes a
-  // whole expert: its rows are read by one XCD, not by all (64 experts of 256
-  // rows, 8192 columns in all: 0.98 ms against 1.10).
+  // Runs of 32 tiles spread every expert over the XCDs.  Where an expert's rows
+  // fit an L2 (4 MiB) and there are many experts, an XCD takes a whole expert,
+  // whose rows are then read by one XCD and not by all (64 experts of 256 rows,
+  // 8192 columns in all: 0.95 ms against 1.08), if the experts have much the
+  // same rows: with rows by a Zipf law of exponent 1.2 the XCD of the largest
+  // takes 1.41 ms, runs of 32 1.05.  The rows are known on the device alone.
   LinearArgs b = a;
-  b.run = avg >= 128 && a.E >= 32 && avg * (a.W + a.H) * 2 <= (4 << 20) ? static_cast<int>(per_expert) : kCusPerXcd;
-  const unsigned blocks = blocks_of(tiles, b.run);
+  b.run = kCusPerXcd;
+  b.even = nullptr;
+  if (a.splits == 1 && avg >= 128 && a.E >= 32 && avg * (a.W + a.H) * 2 <= (4 << 20)) {
+    b.run = static_cast<int>(per_expert);
+    b.even = reinterpret_cast<int32_t*>(a.part);  // no part of split rows lies there
+    k_linear_even<<<1, kBlock, 0, s>>>(a.counts, a.E, b.even, a.status, a.generation);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  // whole rounds of either run
+  const unsigned blocks = blocks_of(blocks_of(tiles, b.run), kCusPerXcd);
   if (half && a.xmap) k_linear<kGradW, 2, true><<<blocks, kThreads, 0, s>>>(b);
   else if (half) k_linear<kGradW, 2, false><<<blocks, kThreads, 0, s>>>(b);
   else if (a.xmap) k_linear<kGradW, 4, true><<<blocks, kThreads, 0, s>>>(b);

@@ -218,6 +218,20 @@ def test_linear_one_expert_has_all_rows():
     check(3000, 1, 40, 72, 40, "relu", gather=True, idx=idx)
 
 
+@pytest.mark.parametrize("rows,N", [("even", 520), ("skewed", 520), ("one", 520), ("split", 40)])
+def test_linear_weight_gradient_orders(rows, N):
+    """32 experts of 160 rows on average, several tiles each: tiles dealt to the
+    XCDs by expert where the rows are even, else in runs; and with rows enough
+    to be split over blocks."""
+    T = 5120 if rows != "split" else 32 * 600
+    e = torch.arange(T) % 32
+    if rows == "skewed":
+        e = torch.where(torch.arange(T) % 3 == 0, torch.full_like(e, 7), e)
+    if rows == "one":
+        e = torch.full_like(e, 30)
+    check(T, 1, 32, 264, N, "relu", gather=rows != "one", idx=e.reshape(T, 1))
+
+
 @pytest.mark.parametrize("gather", [False, True])
 def test_linear_weight_gradient_of_many_rows_is_split(gather):
     """One and two experts with thousands of rows: the rows are split over
