@@ -62,7 +62,6 @@ enum Kind { kForward, kGradX, kGradW };
 // where lanes past the contraction's end load from
 __device__ __align__(16) const uint32_t kZeros[4] = {0u, 0u, 0u, 0u};
 
-
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return static_cast<uint32_t>(
       reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p));
@@ -775,8 +774,8 @@ __global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(Linea
 // Forward where experts have a few rows each (a decoding step: the weights are
 // read once and nothing else counts), or the whole problem is small.  A block
 // takes 64 of an expert's columns (32 gate and 32 up with a gate) and 16 of
-// its rows; its 8 waves take the 128-byte lines of the contraction in turn.  Weights and rows go
-// straight from memory into the operands of v_mfma_f32_16x16x32_bf16 (a
+// its rows; its 8 waves take the 128-byte lines of the contraction in turn.
+// Weights and rows go straight from memory into the operands of v_mfma_f32_16x16x32_bf16 (a
 // load instruction takes 64 bytes of 16 weight rows), a line ahead of the
 // product, so a wave keeps 8 KiB of weights in flight and waits for nobody;
 // the waves' sums meet in LDS at the end, in their order.  16 tokens x 4096 ->
