@@ -75,8 +75,8 @@ LinearGeom linear_geom(int64_t rows, int E, int H, int W);
 int64_t linear_max_tiles(int64_t rows, int E, int H, int W, int splits);
 
 hipError_t launch_linear(const LinearArgs& a, int64_t rows, hipStream_t s);
-hipError_t launch_linear_grad_x(const LinearArgs& a, int64_t rows, hipStream_t s);
-hipError_t launch_linear_grad_w(const LinearArgs& a, int64_t rows, hipStream_t s);
+// grad_x of x and grad_w of w, either null
+hipError_t launch_linear_grads(const LinearArgs* x, const LinearArgs* w, int64_t rows, hipStream_t s);
 hipError_t launch_act_backward(const ActBackwardArgs& a, int64_t rows, hipStream_t s);
 
 // The balance loss.  Tokens are taken in chunks of a fixed size; the part of

@@ -155,7 +155,7 @@ int ep_expert_linear_backward(const ep_problem_t* p, const ep_layout_t* L, const
   a.gb = static_cast<uint16_t*>(grad_bias);
   // no row: the weights' gradients are zero, by the same kernel
   if (p->num_tokens == 0)
-    return !grad_w || ep::launch_linear_grad_w(a, 0, stream) == hipSuccess ? EP_OK : EP_EHIP;
+    return ep::launch_linear_grads(nullptr, grad_w ? &a : nullptr, 0, stream) == hipSuccess ? EP_OK : EP_EHIP;
   int64_t ldgo = 0;
   if ((rc = check_stride(grad_out, grad_out_row_stride, a.N, &ldgo)) != EP_OK) return rc;
   if (grad_w && (rc = check_stride(x, x_row_stride, a.H, &a.ldx)) != EP_OK) return rc;
@@ -207,17 +207,13 @@ int ep_expert_linear_backward(const ep_problem_t* p, const ep_layout_t* L, const
     a.g = static_cast<const uint16_t*>(grad_pre);
     a.ldg = b.ldgpre;
   }
-  if (grad_x) {
-    ep::LinearArgs ax = a;
-    ax.out = static_cast<uint16_t*>(grad_x);
-    if (ep::launch_linear_grad_x(ax, g.rows, stream) != hipSuccess) return EP_EHIP;
-  }
-  if (grad_w) {
-    a.splits = g.splits;
-    a.part = static_cast<float*>(workspace);
-    if (ep::launch_linear_grad_w(a, g.rows, stream) != hipSuccess) return EP_EHIP;
-  }
-  return EP_OK;
+  ep::LinearArgs ax = a;
+  ax.out = static_cast<uint16_t*>(grad_x);
+  a.splits = g.splits;
+  a.part = static_cast<float*>(workspace);
+  return ep::launch_linear_grads(grad_x ? &ax : nullptr, grad_w ? &a : nullptr, g.rows, stream) == hipSuccess
+             ? EP_OK
+             : EP_EHIP;
 }
 
 size_t ep_balance_workspace_bytes(const ep_balance_t* b) {

@@ -226,12 +226,12 @@ struct Tile {
   int split;
 };
 
-// The i-th tile of this block's XCD (blocks are dealt to the 8 XCDs
-// round-robin): runs of `run` tiles, or of an eighth of all if that is less,
+// The tile of a block (blocks are dealt to the 8 XCDs round-robin): runs of `run` tiles, or of an eighth of all if that is less,
 // are dealt to the XCDs in turn, so that tiles side by side share an L2.
-__device__ __forceinline__ int tile_at(int i, int total, int run) {
+__device__ __forceinline__ int tile_at(int block, int total, int run) {
   const int r = min(run, (total + kXcds - 1) / kXcds);
-  return (i / r * kXcds + static_cast<int>(blockIdx.x % kXcds)) * r + i % r;
+  const int i = block / kXcds;
+  return (i / r * kXcds + block % kXcds) * r + i % r;
 }
 
 // Tile `local` of mt x nt: groups of kRowGroup row tiles, within a group
@@ -249,8 +249,14 @@ __device__ __forceinline__ void tile_of(int local, int mt, int nt, int& im, int&
 template <int MI>
 constexpr int kBlocksPerCu = MI == 2 ? 2 : 1;
 
+// bytes of the rings
+template <Kind KIND, int MI>
+constexpr int kRingBytes = KIND == kGradW ? (MI == 2 ? 3 : 4) * (kBK * 64 * MI * 2 + kBN * kBK * 2)
+                                          : 2 * 64 * MI * kXBK * 2 + (MI == 2 ? 3 : 4) * kBN * kBK * 2;
+
+// block `block` of a product, its rings at `lds`
 template <Kind KIND, int MI, bool GATHER>
-__global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(LinearArgs a) {
+__device__ __forceinline__ void linear_block(const LinearArgs& a, const int block, char* const lds) {
   constexpr bool kRowAcross = KIND == kGradW;    // row operand's contraction runs across memory
   constexpr bool kColAcross = KIND != kForward;  // column operand's
   static_assert(!kRowAcross || MI == 2 || MI == 4, "heights of a row operand across memory");
@@ -263,7 +269,7 @@ __global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(Linea
   // the tile table lies in the ring until the first load, the epilogue's
   // slices after the last
   static_assert((1024 + 8) * 4 <= kRing && 8 * 4096 <= kRing, "table and slices fit");
-  __shared__ __align__(1024) char lds[kRing];
+  static_assert(kRing == kRingBytes<KIND, MI>, "rings as allocated");
   char* const sRow = lds;
   char* const sCol = lds + kRowStages * kRowBytes;
   int* const sTiles = reinterpret_cast<int*>(lds);
@@ -287,7 +293,7 @@ __global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(Linea
     const int mt = (a.W + kBM - 1) / kBM;
     const int total = a.E * a.splits * mt * nt;  // below 2^22
     const int run = a.even && *a.even == 0 ? kCusPerXcd : a.run;
-    const int tile = tile_at(static_cast<int>(blockIdx.x / kXcds), total, run);
+    const int tile = tile_at(block, total, run);
     if (tile >= total) return;
     const int es = tile / (mt * nt);
     T.e = es / a.splits;
@@ -315,7 +321,7 @@ __global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(Linea
     // values from LDS are the same in every lane: scalar from here on
     const int total = __builtin_amdgcn_readfirstlane(block_exclusive_scan<kThreads>(sTiles, a.E, sTiles + 1024));
     if (total == 0) return;
-    const int tile = tile_at(static_cast<int>(blockIdx.x / kXcds), total, a.run);
+    const int tile = tile_at(block, total, a.run);
     if (tile >= total) return;
     // the last expert whose first tile is not past it (empty ones repeat the
     // prefix of the next)
@@ -770,6 +776,24 @@ __global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(Linea
   finish();
 }
 
+template <Kind KIND, int MI, bool GATHER>
+__global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(LinearArgs a) {
+  __shared__ __align__(1024) char lds[kRingBytes<KIND, MI>];
+  linear_block<KIND, MI, GATHER>(a, static_cast<int>(blockIdx.x), lds);
+}
+
+// Both gradients in tiles of 128 rows: the first `x_blocks` (a multiple of 8)
+// are grad_x's.  Neither needs the other, and one's blocks fill the CUs that
+// the other's leave.
+template <bool GATHER>
+__global__ __launch_bounds__(kThreads, 4) void k_linear_grads(LinearArgs x, LinearArgs w, int x_blocks) {
+  constexpr int kX = kRingBytes<kGradX, 2>, kW = kRingBytes<kGradW, 2>;
+  __shared__ __align__(1024) char lds[kX > kW ? kX : kW];
+  const int block = static_cast<int>(blockIdx.x);
+  if (block < x_blocks) linear_block<kGradX, 2, false>(x, block, lds);
+  else linear_block<kGradW, 2, GATHER>(w, block - x_blocks, lds);
+}
+
 // ---------------------------------------------------------------- few rows
 // Forward where experts have a few rows each (a decoding step: the weights are
 // read once and nothing else counts), or the whole problem is small.  A block
@@ -800,7 +824,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_linear_few(LinearArgs a) {
   __syncthreads();
   const int total = __builtin_amdgcn_readfirstlane(block_exclusive_scan<kThreads>(sTiles, a.E, sTiles + 1024));
   if (total == 0) return;
-  const int tile = tile_at(static_cast<int>(blockIdx.x / kXcds), total, a.run);
+  const int tile = tile_at(static_cast<int>(blockIdx.x), total, a.run);
   if (tile >= total) return;
   int lo = 0, hi = a.E - 1;  // the last expert whose first tile is not past it
   while (lo < hi) {
@@ -1025,8 +1049,13 @@ unsigned blocks_of(int64_t tiles, int64_t run) {
 
 int64_t row_tiles(int64_t rows, int E, int bm) { return ceil_div(rows, bm) + (rows < E ? rows : E); }
 
-template <Kind KIND, bool GATHER>
-hipError_t launch_rows(const LinearArgs& a, int64_t rows, int64_t nt, hipStream_t s) {
+// Launch shape of a product whose tiles' rows are the experts' rows.
+struct RowPlan {
+  int mi;  // 32-row sub-tiles of a wave: tiles of 64 mi rows
+  int run;
+  unsigned blocks;
+};
+RowPlan plan_rows(const LinearArgs& a, int64_t rows, int64_t nt) {
   // Tile height by the rounds of tiles over the CUs and their height, for rows
   // that the router spread at random: an expert then has its share and about
   // two standard deviations more.
@@ -1052,12 +1081,17 @@ hipError_t launch_rows(const LinearArgs& a, int64_t rows, int64_t nt, hipStream_
   // experts: 1.81 ms, one run an XCD 1.87).  Where weights are read once, one
   // run an XCD streams them faster (64 experts of 4 rows: 260 us against 270;
   // of 64 rows 396 against 459).
+  const int run = best == 2 ? INT_MAX : kCusPerXcd;
+  return {best, run, blocks_of(row_tiles(rows, a.E, 64 * best) * nt, run)};
+}
+
+template <Kind KIND, bool GATHER>
+hipError_t launch_rows(const LinearArgs& a, const RowPlan& plan, hipStream_t s) {
   LinearArgs b = a;
-  b.run = best == 2 ? INT_MAX : kCusPerXcd;
-  const unsigned blocks = blocks_of(row_tiles(rows, a.E, 64 * best) * nt, b.run);
-  if (best == 2) k_linear<KIND, 2, GATHER><<<blocks, kThreads, 0, s>>>(b);
-  else if (best == 4) k_linear<KIND, 4, GATHER><<<blocks, kThreads, 0, s>>>(b);
-  else k_linear<KIND, 5, GATHER><<<blocks, kThreads, 0, s>>>(b);
+  b.run = plan.run;
+  if (plan.mi == 2) k_linear<KIND, 2, GATHER><<<plan.blocks, kThreads, 0, s>>>(b);
+  else if (plan.mi == 4) k_linear<KIND, 4, GATHER><<<plan.blocks, kThreads, 0, s>>>(b);
+  else k_linear<KIND, 5, GATHER><<<plan.blocks, kThreads, 0, s>>>(b);
   return hipGetLastError();
 }
 
@@ -1099,14 +1133,15 @@ hipError_t launch_linear(const LinearArgs& a, int64_t rows, hipStream_t s) {
     return hipGetLastError();
   }
   const int64_t nt = ceil_div(a.N, a.gated ? kBN / 2 : kBN);
-  return a.xmap ? launch_rows<kForward, true>(a, rows, nt, s) : launch_rows<kForward, false>(a, rows, nt, s);
+  const RowPlan plan = plan_rows(a, rows, nt);
+  return a.xmap ? launch_rows<kForward, true>(a, plan, s) : launch_rows<kForward, false>(a, plan, s);
 }
 
-hipError_t launch_linear_grad_x(const LinearArgs& a, int64_t rows, hipStream_t s) {
-  return launch_rows<kGradX, false>(a, rows, ceil_div(a.H, kBN), s);
-}
-
-hipError_t launch_linear_grad_w(const LinearArgs& a, int64_t rows, hipStream_t s) {
+hipError_t launch_linear_grads(const LinearArgs* x, const LinearArgs* w, int64_t rows, hipStream_t s) {
+  RowPlan plan = {};
+  if (x) plan = plan_rows(*x, rows, ceil_div(x->H, kBN));
+  if (!w) return x ? launch_rows<kGradX, false>(*x, plan, s) : hipSuccess;
+  const LinearArgs& a = *w;
   // Where experts have few rows, starting a tile and writing it take the time:
   // 128 x 256 tiles, two blocks a CU (64 experts of 4 rows, 2.1 GB of gradients:
   // 358 us, 256 x 256 tiles 460; of 64 rows 500 and 594; of 256 rows 985 and 948).
@@ -1132,7 +1167,21 @@ hipError_t launch_linear_grad_w(const LinearArgs& a, int64_t rows, hipStream_t s
   }
   // whole rounds of either run
   const unsigned blocks = blocks_of(blocks_of(tiles, b.run), kCusPerXcd);
-  if (half && a.xmap) k_linear<kGradW, 2, true><<<blocks, kThreads, 0, s>>>(b);
+  // One launch for both where both take tiles of 128 rows (509 rows x 1032 ->
+  // 520, top-2 of 8: 31.2 -> 23.3 us in all; 255 x 2376 -> 920, top-2 of 38: 103
+  // -> 91; no shape slower).
+  const bool both = x && plan.mi == 2 && half && plan.blocks + blocks < (1u << 22);
+  if (x && !both) {
+    const hipError_t e = launch_rows<kGradX, false>(*x, plan, s);
+    if (e != hipSuccess) return e;
+  }
+  if (both) {
+    LinearArgs c = *x;
+    c.run = plan.run;
+    const int x_blocks = static_cast<int>(plan.blocks);
+    if (a.xmap) k_linear_grads<true><<<plan.blocks + blocks, kThreads, 0, s>>>(c, b, x_blocks);
+    else k_linear_grads<false><<<plan.blocks + blocks, kThreads, 0, s>>>(c, b, x_blocks);
+  } else if (half && a.xmap) k_linear<kGradW, 2, true><<<blocks, kThreads, 0, s>>>(b);
   else if (half) k_linear<kGradW, 2, false><<<blocks, kThreads, 0, s>>>(b);
   else if (a.xmap) k_linear<kGradW, 4, true><<<blocks, kThreads, 0, s>>>(b);
   else k_linear<kGradW, 4, false><<<blocks, kThreads, 0, s>>>(b);

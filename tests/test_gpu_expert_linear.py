@@ -332,6 +332,33 @@ def test_linear_in_place_and_partial_gradients():
     assert only_w[0] is None and only_w[2] is None and torch.equal(only_w[1], full[1])
 
 
+@pytest.mark.parametrize("T,K,E,H,N,gather", [
+    (40, 2, 8, 264, 120, False),     # a few rows an expert
+    (300, 2, 8, 1032, 520, True),    # about 70
+    (1100, 1, 4, 520, 1288, False),  # about 270
+    (4000, 2, 33, 264, 520, True),   # about 240, many experts
+    (3000, 1, 1, 264, 264, False),   # one expert, rows split
+])
+def test_linear_gradients_together_equal_each_alone(T, K, E, H, N, gather):
+    print(f"together T={T} K={K} E={E} H={H} N={N} gather={gather}", flush=True)
+    m = ep()
+    idx, _ = W.make_routing(W.Workload("x", T=T, H=H, K=K, E=E, mask_p=0.1, seed=T + 1))
+    L = m.ep_layout(idx.to(DEV), E, expert_row_src=True)
+    rows = L.max_expert_rows()
+    g = torch.Generator().manual_seed(T)
+    x, go = bf(g, 1.0, T if gather else rows, H).to(DEV), bf(g, 1.0, rows, N).to(DEV)
+    w = bf(g, H**-0.5, E, N, H).to(DEV)
+    kw = dict(gather=gather)
+    gx, gw, gb, _ = m.ep_expert_linear_backward(go, x, L, w, bias=True, grad_x=marked(rows, H), **kw)
+    ax, none, _, _ = m.ep_expert_linear_backward(go, x, L, w, grad_x=marked(rows, H), needs=(True, False), **kw)
+    assert none is None
+    none, aw, ab, _ = m.ep_expert_linear_backward(go, x, L, w, bias=True, needs=(False, True), **kw)
+    assert none is None
+    torch.cuda.synchronize()
+    assert np.array_equal(u16(gx), u16(ax))
+    assert np.array_equal(u16(gw), u16(aw)) and np.array_equal(u16(gb), u16(ab))
+
+
 def test_linear_stale_empty_and_refused():
     m = ep()
     w = W.Workload("s", T=20, H=64, K=1, E=2, seed=9)
