@@ -782,16 +782,16 @@ __global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MI>) void k_linear(Linea
   linear_block<KIND, MI, GATHER>(a, static_cast<int>(blockIdx.x), lds);
 }
 
-// Both gradients in tiles of 128 rows: the first `x_blocks` (a multiple of 8)
-// are grad_x's.  Neither needs the other, and one's blocks fill the CUs that
-// the other's leave.
-template <bool GATHER>
-__global__ __launch_bounds__(kThreads, 4) void k_linear_grads(LinearArgs x, LinearArgs w, int x_blocks) {
-  constexpr int kX = kRingBytes<kGradX, 2>, kW = kRingBytes<kGradW, 2>;
+// Both gradients: the first `x_blocks` (a multiple of 8) are grad_x's.  Neither
+// needs the other, and one's blocks fill the CUs that the other's leave.
+template <int MX, int MW, bool GATHER>
+__global__ __launch_bounds__(kThreads, 2 * kBlocksPerCu<MX>) void k_linear_grads(LinearArgs x, LinearArgs w, int x_blocks) {
+  static_assert(kBlocksPerCu<MX> == kBlocksPerCu<MW>, "tiles of one occupancy");
+  constexpr int kX = kRingBytes<kGradX, MX>, kW = kRingBytes<kGradW, MW>;
   __shared__ __align__(1024) char lds[kX > kW ? kX : kW];
   const int block = static_cast<int>(blockIdx.x);
-  if (block < x_blocks) linear_block<kGradX, 2, false>(x, block, lds);
-  else linear_block<kGradW, 2, GATHER>(w, block - x_blocks, lds);
+  if (block < x_blocks) linear_block<kGradX, MX, false>(x, block, lds);
+  else linear_block<kGradW, MW, GATHER>(w, block - x_blocks, lds);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -1170,7 +1170,7 @@ hipError_t launch_linear_grads(const LinearArgs* x, const LinearArgs* w, int64_t
   // One launch for both where both take tiles of 128 rows (509 rows x 1032 ->
   // 520, top-2 of 8: 31.2 -> 23.3 us in all; 255 x 2376 -> 920, top-2 of 38: 103
   // -> 91; no shape slower).
-  const bool both = x && plan.mi == 2 && half && plan.blocks + blocks < (1u << 22);
+  const bool both = x && (plan.mi == 2) == half && plan.blocks + blocks < (1u << 22);
   if (x && !both) {
     const hipError_t e = launch_rows<kGradX, false>(*x, plan, s);
     if (e != hipSuccess) return e;
@@ -1179,8 +1179,17 @@ hipError_t launch_linear_grads(const LinearArgs* x, const LinearArgs* w, int64_t
     LinearArgs c = *x;
     c.run = plan.run;
     const int x_blocks = static_cast<int>(plan.blocks);
-    if (a.xmap) k_linear_grads<true><<<plan.blocks + blocks, kThreads, 0, s>>>(c, b, x_blocks);
-    else k_linear_grads<false><<<plan.blocks + blocks, kThreads, 0, s>>>(c, b, x_blocks);
+#define EP_GRADS(MX, MW)                                                                                   \
+  if (a.xmap) k_linear_grads<MX, MW, true><<<plan.blocks + blocks, kThreads, 0, s>>>(c, b, x_blocks);       \
+  else k_linear_grads<MX, MW, false><<<plan.blocks + blocks, kThreads, 0, s>>>(c, b, x_blocks);
+    if (half) {
+      EP_GRADS(2, 2)
+    } else if (plan.mi == 4) {
+      EP_GRADS(4, 4)
+    } else {
+      EP_GRADS(5, 4)
+    }
+#undef EP_GRADS
   } else if (half && a.xmap) k_linear<kGradW, 2, true><<<blocks, kThreads, 0, s>>>(b);
   else if (half) k_linear<kGradW, 2, false><<<blocks, kThreads, 0, s>>>(b);
   else if (a.xmap) k_linear<kGradW, 4, true><<<blocks, kThreads, 0, s>>>(b);
