@@ -1145,8 +1145,11 @@ hipError_t launch_linear_grads(const LinearArgs* x, const LinearArgs* w, int64_t
   // Where experts have few rows, starting a tile and writing it take the time:
   // 128 x 256 tiles, two blocks a CU (64 experts of 4 rows, 2.1 GB of gradients:
   // 358 us, 256 x 256 tiles 460; of 64 rows 500 and 594; of 256 rows 985 and 948).
+  // So too where grad_x has few tiles and takes those, for one launch of both
+  // (8 experts of 260 rows, 1712 -> 2440: 90 -> 59 us; 4 of 500, 1024 -> 1024: 42
+  // -> 24; 61 of 197, 520 -> 264: 36.7 -> 37.3).
   const int64_t avg = rows / a.E;
-  const bool half = avg <= 128;
+  const bool half = avg <= 128 || (x && plan.mi == 2);
   const int64_t per_expert = ceil_div(a.W, half ? 128 : 256) * ceil_div(a.H, kBN) * a.splits;
   const int64_t tiles = per_expert * a.E;
   // Runs of 32 tiles spread every expert over the XCDs.  Where an expert's rows
@@ -1167,9 +1170,9 @@ hipError_t launch_linear_grads(const LinearArgs* x, const LinearArgs* w, int64_t
   }
   // whole rounds of either run
   const unsigned blocks = blocks_of(blocks_of(tiles, b.run), kCusPerXcd);
-  // One launch for both where both take tiles of 128 rows (509 rows x 1032 ->
-  // 520, top-2 of 8: 31.2 -> 23.3 us in all; 255 x 2376 -> 920, top-2 of 38: 103
-  // -> 91; no shape slower).
+  // One launch for both (509 rows x 1032 -> 520, top-2 of 8: 31.2 -> 23.3 us in
+  // all; 64 experts by a Zipf law of 1.2: 1870 -> 1785; 32 experts of 2048 rows,
+  // 2048 -> 7168: 3.86 -> 3.88 ms), where the blocks of both have one occupancy.
   const bool both = x && (plan.mi == 2) == half && plan.blocks + blocks < (1u << 22);
   if (x && !both) {
     const hipError_t e = launch_rows<kGradX, false>(*x, plan, s);
