@@ -147,17 +147,23 @@ def test_linear_backward_refusals():
 
 def test_linear_workspace_to_the_byte():
     """As the kernels index it: S parts of fp32 [E, W, H] and, behind them, of
-    [E, W]; S parts only where 256 rows an even share are left each and the
-    tiles do not fill the chip twice."""
+    [E, W]; S at its least cost in us, with 64 rows an even share left each and
+    no more blocks than fill the chip twice."""
     rng = random.Random(2)
     for _ in range(400):
         T, K, E = rng.randint(1, 20000), rng.randint(1, 4), rng.randint(1, 40)
         H, N, gated = 8 * rng.randint(1, 300), 8 * rng.randint(1, 300), rng.randint(0, 1)
         W = N * (1 + gated)
         tiles = -(-W // 256) * -(-H // 256) * E
-        S = max(1, min(512 // tiles if tiles < 512 else 1, T * K // E // 256))
         p, lin = _problem(T=T, H=H, K=min(K, E), E=E), _linear(n_out=N, gated=gated)
-        S = max(1, min(512 // tiles if tiles < 512 else 1, T * min(K, E) // E // 256))
+        rows = T * min(K, E)
+
+        def cost(s):
+            steps = -(-(-(-rows // (E * s))) // 32)
+            c = float(-(-tiles * s // 256)) * (0.9 * float(steps) + 8.0)
+            return c + (5.0 + 8.0 * float((W * H + W) * E * s) / 6.0e6) if s > 1 else c
+
+        S = min((s for s in range(1, 513) if s == 1 or (s * tiles <= 512 and 64 * s <= rows // E)), key=cost)
         want = S * E * W * (H + 1) * 4 if S > 1 else 16
         got = _lib.lib().ep_expert_linear_workspace_bytes(ctypes.byref(p), ctypes.byref(lin))
         assert got == want
