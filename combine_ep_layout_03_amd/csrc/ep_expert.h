@@ -72,7 +72,7 @@ struct LinearGeom {
 };
 LinearGeom linear_geom(int64_t rows, int E, int H, int W);
 // tiles of the largest launch of these sizes, at most
-int64_t linear_max_tiles(int64_t rows, int E, int H, int W, int splits);
+int64_t linear_max_tiles(int64_t rows, int E, int H, int W);
 
 hipError_t launch_linear(const LinearArgs& a, int64_t rows, hipStream_t s);
 // grad_x of x and grad_w of w, either null

@@ -34,11 +34,9 @@ int check_linear(const ep_problem_t* p, const ep_linear_t* lin) {
   if (p->hidden % 8 != 0 || lin->n_out % 8 != 0) return EP_ENOTSUP;
   const int64_t W = lin->gated ? 2LL * lin->n_out : lin->n_out;
   if (p->hidden > kMaxWidth || W > kMaxWidth || W * p->hidden > INT32_MAX) return EP_ENOTSUP;
-  const ep::LinearGeom g = ep::linear_geom(max_rows(p), p->num_experts, p->hidden, static_cast<int>(W));
   // fewer than 2^32 threads in 512 a block, the rounds that a launch is filled up to included
-  if (ep::linear_max_tiles(g.rows, p->num_experts, p->hidden, static_cast<int>(W), g.splits) >= (1 << 22))
-    return EP_ENOTSUP;
-  return EP_OK;
+  return ep::linear_max_tiles(max_rows(p), p->num_experts, p->hidden, static_cast<int>(W)) < (1 << 22) ? EP_OK
+                                                                                                    : EP_ENOTSUP;
 }
 
 int check_stride(const void* p, int64_t stride, int32_t width, int64_t* ld) {

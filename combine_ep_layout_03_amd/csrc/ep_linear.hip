@@ -1109,7 +1109,7 @@ LinearGeom linear_geom(int64_t rows, int E, int H, int W) {
   constexpr int64_t kCus = kXcds * kCusPerXcd;
   g.splits = 1;
   double least = 0.0;
-  for (int64_t s = 1; s == 1 || (s * tiles <= 2 * kCus && s * 64 <= rows / E); ++s) {
+  for (int64_t s = 1; s == 1 || (s * tiles <= 2 * kCus && s * 64 <= rows / E); s += s < 8 ? 1 : s / 8) {
     const int64_t steps = ceil_div(ceil_div(rows, E * s), kBK);
     double cost = static_cast<double>(ceil_div(tiles * s, kCus)) * (0.9 * static_cast<double>(steps) + 8.0);
     if (s > 1) cost += 5.0 + 8.0 * static_cast<double>((static_cast<int64_t>(W) * H + W) * E * s) / 6.0e6;
@@ -1122,10 +1122,11 @@ LinearGeom linear_geom(int64_t rows, int E, int H, int W) {
   return g;
 }
 
-int64_t linear_max_tiles(int64_t rows, int E, int H, int W, int splits) {
+int64_t linear_max_tiles(int64_t rows, int E, int H, int W) {
   // columns of 128 (gated) or 256, rows of 128 at least
   const int64_t by_rows = row_tiles(rows, E, 128) * ceil_div(W > H ? W : H, 128);
-  const int64_t by_weights = ceil_div(W, 128) * ceil_div(H, kBN) * E * splits;
+  // (rows are split where that makes no more than 1024)
+  const int64_t by_weights = ceil_div(W, 128) * ceil_div(H, kBN) * E;
   const int64_t few = rows <= 4 * static_cast<int64_t>(E) ? row_tiles(rows, E, 16) * ceil_div(W, 64) : 0;
   const int64_t tiles = by_rows > by_weights ? by_rows : by_weights;
   return few > tiles ? few : tiles;

@@ -163,7 +163,11 @@ def test_linear_workspace_to_the_byte():
             c = float(-(-tiles * s // 256)) * (0.9 * float(steps) + 8.0)
             return c + (5.0 + 8.0 * float((W * H + W) * E * s) / 6.0e6) if s > 1 else c
 
-        S = min((s for s in range(1, 513) if s == 1 or (s * tiles <= 512 and 64 * s <= rows // E)), key=cost)
+        tried, s = [], 1
+        while s == 1 or (s * tiles <= 512 and 64 * s <= rows // E):
+            tried.append(s)
+            s += 1 if s < 8 else s // 8
+        S = min(tried, key=cost)
         want = S * E * W * (H + 1) * 4 if S > 1 else 16
         got = _lib.lib().ep_expert_linear_workspace_bytes(ctypes.byref(p), ctypes.byref(lin))
         assert got == want
