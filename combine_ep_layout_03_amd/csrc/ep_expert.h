@@ -64,16 +64,6 @@ struct ActBackwardArgs {
   uint32_t generation;
 };
 
-// Launch geometry of the layer's gradients, from the sizes alone.
-struct LinearGeom {
-  int64_t rows;  // expert-major rows at most, padding included
-  int splits;    // parts of each expert's rows in the weight gradient
-  size_t part_bytes;  // of workspace, 16 at least
-};
-LinearGeom linear_geom(int64_t rows, int E, int H, int W);
-// tiles of the largest launch of these sizes, at most
-int64_t linear_max_tiles(int64_t rows, int E, int H, int W);
-
 hipError_t launch_linear(const LinearArgs& a, int64_t rows, hipStream_t s);
 // grad_x of x and grad_w of w, either null
 hipError_t launch_linear_grads(const LinearArgs* x, const LinearArgs* w, int64_t rows, hipStream_t s);

@@ -8,6 +8,7 @@
 
 #include "ep_checks.h"
 #include "ep_expert.h"
+#include "ep_linear_plan.h"
 
 using namespace ep::checks;
 
@@ -167,14 +168,15 @@ int ep_expert_linear_backward(const ep_problem_t* p, const ep_layout_t* L, const
     if ((rc = check_stride(grad_pre, grad_pre_row_stride, a.W, &b.ldgpre)) != EP_OK) return rc;
   }
   if (a.xmap && grad_w && p->num_tokens * a.ldx * 2 > kMaxGather) return EP_ENOTSUP;
-  const ep::LinearGeom g = ep::linear_geom(max_rows(p), a.E, a.H, a.W);
+  const int64_t rows = max_rows(p);
+  const ep::LinearGeom g = ep::linear_geom(rows, a.E, a.H, a.W);
   const int64_t nw = 2LL * a.E * a.W * a.H, nb = 2LL * a.E * a.W;
-  const Rows ro = {grad_out, g.rows, 2LL * a.N, 2 * ldgo};
-  const Rows rx = {grad_w ? x : nullptr, a.xmap ? p->num_tokens : g.rows, 2LL * a.H, 2 * a.ldx};
+  const Rows ro = {grad_out, rows, 2LL * a.N, 2 * ldgo};
+  const Rows rx = {grad_w ? x : nullptr, a.xmap ? p->num_tokens : rows, 2LL * a.H, 2 * a.ldx};
   const Rows rw = {grad_x ? lin->w : nullptr, 1, nw, nw};
-  const Rows rp = {pre, pre ? g.rows : 0, 2LL * a.W, 2 * b.ldpre};
-  const Rows gp = {grad_pre, grad_pre ? g.rows : 0, 2LL * a.W, 2 * b.ldgpre};
-  const Rows gx = {grad_x, grad_x ? g.rows : 0, 2LL * a.H, 2 * a.ldout};
+  const Rows rp = {pre, pre ? rows : 0, 2LL * a.W, 2 * b.ldpre};
+  const Rows gp = {grad_pre, grad_pre ? rows : 0, 2LL * a.W, 2 * b.ldgpre};
+  const Rows gx = {grad_x, grad_x ? rows : 0, 2LL * a.H, 2 * a.ldout};
   const Rows gw = {grad_w, grad_w ? 1 : 0, nw, nw}, gb = {grad_bias, grad_bias ? 1 : 0, nb, nb};
   if (any_overlap(gp, {ro, rx, rw, gx, gw, gb}) || any_overlap(gx, {ro, rx, rw, rp, gw, gb}) ||
       any_overlap(gw, {ro, rx, rw, rp, gb}) || any_overlap(gb, {ro, rx, rw, rp}))
@@ -201,7 +203,7 @@ int ep_expert_linear_backward(const ep_problem_t* p, const ep_layout_t* L, const
     b.padded = p->expert_alignment > 1;
     b.status = a.status;
     b.generation = a.generation;
-    if (ep::launch_act_backward(b, g.rows, stream) != hipSuccess) return EP_EHIP;
+    if (ep::launch_act_backward(b, rows, stream) != hipSuccess) return EP_EHIP;
     a.g = static_cast<const uint16_t*>(grad_pre);
     a.ldg = b.ldgpre;
   }
@@ -209,7 +211,7 @@ int ep_expert_linear_backward(const ep_problem_t* p, const ep_layout_t* L, const
   ax.out = static_cast<uint16_t*>(grad_x);
   a.splits = g.splits;
   a.part = static_cast<float*>(workspace);
-  return ep::launch_linear_grads(grad_x ? &ax : nullptr, grad_w ? &a : nullptr, g.rows, stream) == hipSuccess
+  return ep::launch_linear_grads(grad_x ? &ax : nullptr, grad_w ? &a : nullptr, rows, stream) == hipSuccess
              ? EP_OK
              : EP_EHIP;
 }

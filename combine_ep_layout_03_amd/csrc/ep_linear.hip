@@ -36,10 +36,8 @@
 // they store (weight gradients of 256 rows an expert 1.12 ms against 1.09: a
 // wave's stores and loads retire in one order, so its loads wait for its
 // stores).
-#include <limits.h>
-#include <math.h>
-
 #include "ep_expert.h"
+#include "ep_linear_plan.h"
 
 namespace ep {
 
@@ -50,11 +48,9 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 512;
-constexpr int kBN = 256;     // columns of a tile
-constexpr int kBK = 32;      // contraction step
+constexpr int kBN = kTileCols;
+constexpr int kBK = kTileStep;
 constexpr int kXBK = 2 * kBK;  // stage of a row operand that runs along memory (whole lines)
-constexpr int kXcds = 8;
-constexpr int kCusPerXcd = 32;
 constexpr int kRowGroup = 8;  // row tiles that share a run of column tiles
 
 enum Kind { kForward, kGradX, kGradW };
@@ -1038,55 +1034,8 @@ __global__ __launch_bounds__(kBlock) void k_act_backward(ActBackwardArgs a) {
   }
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Blocks of a launch with up to `tiles` tiles in runs of `run`: whole rounds
-// of runs over the XCDs, or of an eighth of the tiles.
-unsigned blocks_of(int64_t tiles, int64_t run) {
-  if (run > ceil_div(tiles, kXcds)) run = ceil_div(tiles, kXcds);
-  return static_cast<unsigned>(ceil_div(tiles, kXcds * run) * kXcds * run);
-}
-
-int64_t row_tiles(int64_t rows, int E, int bm) { return ceil_div(rows, bm) + (rows < E ? rows : E); }
-
-// Launch shape of a product whose tiles' rows are the experts' rows.
-struct RowPlan {
-  int mi;  // 32-row sub-tiles of a wave: tiles of 64 mi rows
-  int run;
-  unsigned blocks;
-};
-RowPlan plan_rows(const LinearArgs& a, int64_t rows, int64_t nt) {
-  // Tile height by the rounds of tiles over the CUs and their height, for rows
-  // that the router spread at random: an expert then has its share and about
-  // two standard deviations more.
-  const double avg = static_cast<double>(rows) / a.E;
-  const double most = avg + 2.0 * sqrt(avg * (a.E - 1) / a.E);
-  int best = 0;
-  double least = 0.0;
-  for (int mi : {2, 4, 5}) {
-    const int64_t mt = ceil_div(static_cast<int64_t>(ceil(most)), 64 * mi);
-    const double per = static_cast<double>(ceil_div(ceil_div(static_cast<int64_t>(ceil(most)), mt), 32) * 32);
-    // two blocks of 128 rows share a CU
-    const int64_t places = kXcds * kCusPerXcd * (mi == 2 ? 2 : 1);
-    const int64_t tiles = mt * a.E * nt;
-    const int64_t turns = ceil_div(tiles, places) * (mi == 2 && tiles > places / 2 ? 2 : 1);
-    const double cost = static_cast<double>(turns) * (per + 64.0);
-    if (best == 0 || cost < least) {
-      best = mi;
-      least = cost;
-    }
-  }
-  // Runs of 32, one tile a CU: all XCDs work on neighbouring tiles, whose rows
-  // and weights meet in the memory-side cache (65,536 rows x 7168 -> 2048 of 32
-  // experts: 1.81 ms, one run an XCD 1.87).  Where weights are read once, one
-  // run an XCD streams them faster (64 experts of 4 rows: 260 us against 270;
-  // of 64 rows 396 against 459).
-  const int run = best == 2 ? INT_MAX : kCusPerXcd;
-  return {best, run, blocks_of(row_tiles(rows, a.E, 64 * best) * nt, run)};
-}
-
 template <Kind KIND, bool GATHER>
-hipError_t launch_rows(const LinearArgs& a, const RowPlan& plan, hipStream_t s) {
+hipError_t launch_rows(const LinearArgs& a, const LinearPlan& plan, hipStream_t s) {
   LinearArgs b = a;
   b.run = plan.run;
   if (plan.mi == 2) k_linear<KIND, 2, GATHER><<<plan.blocks, kThreads, 0, s>>>(b);
@@ -1097,110 +1046,47 @@ hipError_t launch_rows(const LinearArgs& a, const RowPlan& plan, hipStream_t s) 
 
 }  // namespace
 
-LinearGeom linear_geom(int64_t rows, int E, int H, int W) {
-  LinearGeom g;
-  g.rows = rows;
-  const int64_t tiles = ceil_div(W, 256) * ceil_div(H, kBN) * E;
-  // Rows in as many parts as cost least, in us as measured for even rows: 8 a
-  // tile and 0.9 for every 32 of its rows, a tile a CU at once, against writing
-  // and reading the fp32 parts at 6 TB/s and 5 for the join.  (2048 rows x 2048
-  // -> 2048 of one expert: 56.6 us whole, 42.6 in 4 parts, 64.8 in 8; 16,384 x
-  // 1024 -> 1024: 399 whole, 55.6 in 16; 8192 x 4096 -> 4096: 233 whole, 280 in 2.)
-  constexpr int64_t kCus = kXcds * kCusPerXcd;
-  g.splits = 1;
-  double least = 0.0;
-  for (int64_t s = 1; s == 1 || (s * tiles <= 2 * kCus && s * 64 <= rows / E); s += s < 8 ? 1 : s / 8) {
-    const int64_t steps = ceil_div(ceil_div(rows, E * s), kBK);
-    double cost = static_cast<double>(ceil_div(tiles * s, kCus)) * (0.9 * static_cast<double>(steps) + 8.0);
-    if (s > 1) cost += 5.0 + 8.0 * static_cast<double>((static_cast<int64_t>(W) * H + W) * E * s) / 6.0e6;
-    if (s == 1 || cost < least) {
-      least = cost;
-      g.splits = static_cast<int>(s);
-    }
-  }
-  g.part_bytes = g.splits > 1 ? (static_cast<size_t>(W) * H + W) * E * g.splits * 4 : 16;
-  return g;
-}
-
-int64_t linear_max_tiles(int64_t rows, int E, int H, int W) {
-  // columns of 128 (gated) or 256, rows of 128 at least
-  const int64_t by_rows = row_tiles(rows, E, 128) * ceil_div(W > H ? W : H, 128);
-  // (rows are split where that makes no more than 1024)
-  const int64_t by_weights = ceil_div(W, 128) * ceil_div(H, kBN) * E;
-  const int64_t few = rows <= 4 * static_cast<int64_t>(E) ? row_tiles(rows, E, 16) * ceil_div(W, 64) : 0;
-  const int64_t tiles = by_rows > by_weights ? by_rows : by_weights;
-  return few > tiles ? few : tiles;
-}
-
 hipError_t launch_linear(const LinearArgs& a, int64_t rows, hipStream_t s) {
-  // Up to 4 rows an expert, or few enough 16 x 64 pieces that the tiles of
-  // 128 rows and more would leave most CUs idle (8 experts of 127 rows, 1032 ->
-  // 520: 13.5 us against 24; 64 of 16 rows, 4096 -> 2 x 2048: 432 against 381)
-  const int64_t few_nt = ceil_div(a.N, a.gated ? 32 : 64);
-  if (rows <= 4 * static_cast<int64_t>(a.E) || ceil_div(ceil_div(rows, a.E), 16) * a.E * few_nt <= 1024) {
-    LinearArgs b = a;
-    b.run = INT_MAX;
-    const unsigned blocks = blocks_of(row_tiles(rows, a.E, 16) * few_nt, b.run);
-    if (a.xmap) k_linear_few<true><<<blocks, kThreads, 0, s>>>(b);
-    else k_linear_few<false><<<blocks, kThreads, 0, s>>>(b);
-    return hipGetLastError();
-  }
-  const int64_t nt = ceil_div(a.N, a.gated ? kBN / 2 : kBN);
-  const RowPlan plan = plan_rows(a, rows, nt);
-  return a.xmap ? launch_rows<kForward, true>(a, plan, s) : launch_rows<kForward, false>(a, plan, s);
+  const LinearPlan plan = plan_forward(rows, a.E, a.N, a.gated);
+  if (plan.mi != 0) return a.xmap ? launch_rows<kForward, true>(a, plan, s) : launch_rows<kForward, false>(a, plan, s);
+  LinearArgs b = a;
+  b.run = plan.run;
+  if (a.xmap) k_linear_few<true><<<plan.blocks, kThreads, 0, s>>>(b);
+  else k_linear_few<false><<<plan.blocks, kThreads, 0, s>>>(b);
+  return hipGetLastError();
 }
 
 hipError_t launch_linear_grads(const LinearArgs* x, const LinearArgs* w, int64_t rows, hipStream_t s) {
-  RowPlan plan = {};
-  if (x) plan = plan_rows(*x, rows, ceil_div(x->H, kBN));
-  if (!w) return x ? launch_rows<kGradX, false>(*x, plan, s) : hipSuccess;
+  if (!x && !w) return hipSuccess;
+  const LinearArgs& any = w ? *w : *x;
+  const GradsPlan plan = plan_grads(rows, any.E, any.H, any.W, w ? w->splits : 1, x != nullptr, w != nullptr);
+  if (!w) return launch_rows<kGradX, false>(*x, plan.x, s);
   const LinearArgs& a = *w;
-  // Where experts have few rows, starting a tile and writing it take the time:
-  // 128 x 256 tiles, two blocks a CU (64 experts of 4 rows, 2.1 GB of gradients:
-  // 358 us, 256 x 256 tiles 460; of 64 rows 500 and 594; of 256 rows 985 and 948).
-  // So too where grad_x has few tiles and takes those, for one launch of both
-  // (8 experts of 260 rows, 1712 -> 2440: 90 -> 59 us; 4 of 500, 1024 -> 1024: 42
-  // -> 24; 61 of 197, 520 -> 264: 36.7 -> 37.3).
-  const int64_t avg = rows / a.E;
-  const bool half = avg <= 128 || (x && plan.mi == 2);
-  const int64_t per_expert = ceil_div(a.W, half ? 128 : 256) * ceil_div(a.H, kBN) * a.splits;
-  const int64_t tiles = per_expert * a.E;
-  // Runs of 32 tiles spread every expert over the XCDs.  Where an expert's rows
-  // fit an L2 (4 MiB) and there are many experts, an XCD takes a whole expert,
-  // whose rows are then read by one XCD and not by all (64 experts of 256 rows,
-  // 8192 columns in all: 0.95 ms against 1.08), if the experts have much the
-  // same rows: with rows by a Zipf law of exponent 1.2 the XCD of the largest
-  // takes 1.41 ms, runs of 32 1.05.  The rows are known on the device alone.
   LinearArgs b = a;
-  b.run = kCusPerXcd;
+  b.run = plan.w.run;
   b.even = nullptr;
-  if (a.splits == 1 && avg >= 128 && a.E >= 32 && avg * (a.W + a.H) * 2 <= (4 << 20)) {
-    b.run = static_cast<int>(per_expert);
+  if (plan.by_expert) {
     b.even = reinterpret_cast<int32_t*>(a.part);  // no part of split rows lies there
     k_linear_even<<<1, kBlock, 0, s>>>(a.counts, a.E, b.even, a.status, a.generation);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  // whole rounds of either run
-  const unsigned blocks = blocks_of(blocks_of(tiles, b.run), kCusPerXcd);
-  // One launch for both (509 rows x 1032 -> 520, top-2 of 8: 31.2 -> 23.3 us in
-  // all; 64 experts by a Zipf law of 1.2: 1870 -> 1785; 32 experts of 2048 rows,
-  // 2048 -> 7168: 3.86 -> 3.88 ms), where the blocks of both have one occupancy.
-  const bool both = x && (plan.mi == 2) == half && plan.blocks + blocks < (1u << 22);
-  if (x && !both) {
-    const hipError_t e = launch_rows<kGradX, false>(*x, plan, s);
+  if (x && !plan.together) {
+    const hipError_t e = launch_rows<kGradX, false>(*x, plan.x, s);
     if (e != hipSuccess) return e;
   }
-  if (both) {
+  const unsigned blocks = plan.w.blocks;
+  const bool half = plan.w.mi == 2;
+  if (plan.together) {
     LinearArgs c = *x;
-    c.run = plan.run;
-    const int x_blocks = static_cast<int>(plan.blocks);
-#define EP_GRADS(MX, MW)                                                                                   \
-  if (a.xmap) k_linear_grads<MX, MW, true><<<plan.blocks + blocks, kThreads, 0, s>>>(c, b, x_blocks);       \
-  else k_linear_grads<MX, MW, false><<<plan.blocks + blocks, kThreads, 0, s>>>(c, b, x_blocks);
+    c.run = plan.x.run;
+    const int x_blocks = static_cast<int>(plan.x.blocks);
+#define EP_GRADS(MX, MW)                                                                                     \
+  if (a.xmap) k_linear_grads<MX, MW, true><<<plan.x.blocks + blocks, kThreads, 0, s>>>(c, b, x_blocks);       \
+  else k_linear_grads<MX, MW, false><<<plan.x.blocks + blocks, kThreads, 0, s>>>(c, b, x_blocks);
     if (half) {
       EP_GRADS(2, 2)
-    } else if (plan.mi == 4) {
+    } else if (plan.x.mi == 4) {
       EP_GRADS(4, 4)
     } else {
       EP_GRADS(5, 4)
