@@ -190,7 +190,7 @@ __global__ __launch_bounds__(kBlock) void k_balance(BalanceArgs a, int chunk) {
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int g = lane & (LPT - 1);
   const LT* logits = static_cast<const LT*>(a.logits);
-  if (blockIdx.x == 0 && tid == 0) *a.total = 0;  // for the join
+  if (blockIdx.x == 0 && tid == 0) *a.done = 0;  // for the join
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * chunk;
   const int64_t t1 = t0 + chunk < a.T ? t0 + chunk : a.T;
   for (int b = sequence_at(a, t0); b < a.B; ++b) {
@@ -267,25 +267,30 @@ __global__ __launch_bounds__(kBlock) void k_balance(BalanceArgs a, int chunk) {
   }
 }
 
-// The join's word: how many blocks have added their part of the loss, in the
-// bits above kCountShift, and the sum of the parts as a whole number of
-// 2^-kFraction.  Whole numbers add up to the same in any order, and the block
-// that finds all others counted has the sum in its hand: no other memory has
-// to be ordered between blocks.  (A ticket with fences, each of which writes
-// back an L2, took 18 us for 256 blocks.)  A part is at most E <= 2^10, as is
-// their sum: 2^10 blocks at most leave 53 bits of sum, 42 of them fraction, so
-// the sum is off by 2^10 * 2^-43 at most.
+// A block's part of the loss, as a double, goes into two words of the workspace
+// that no other block reads or writes: the block's first item is (b, 16 columns),
+// and the first slot of sequence b (going by where b begins, if it is empty) has
+// a sum and a count for the first of those columns, which only this item reads.
 constexpr int kMaxJoins = 1024;
-constexpr int kCountShift = 53;
-constexpr int kFraction = 42;
+__device__ __forceinline__ int64_t part_at(const BalanceArgs& a, int chunk, int cols, int block) {
+  const int b = block / cols;
+  return (offset_of(a, b) / chunk + b) * a.E + block % cols * kJoinCols;
+}
 
 // Item (b, 16 columns): the slots of sequence b added up, 32 runs of slots
-// side by side and then the runs, and the columns' part of the loss.
+// side by side and then the runs, and the columns' part of the loss.  The block
+// that finishes last adds the parts in their order.  Parts and ticket are
+// read-modify-write atomics, which are carried out where all XCDs see them, and
+// a block waits for its part's before it takes its ticket: no other memory has
+// to be ordered between blocks.  (With fences, each of which writes back an L2,
+// the ticket took 18 us for 256 blocks.)
 __global__ __launch_bounds__(kJoinThreads) void k_balance_join(BalanceArgs a, int chunk, int cols) {
   constexpr int kRuns = kJoinThreads / kJoinCols;
   __shared__ float s_sum[kRuns][kJoinCols];
   __shared__ int s_count[kRuns][kJoinCols];
   __shared__ int s_tokens[kRuns];
+  __shared__ double s_part[kJoinThreads / kWave];
+  __shared__ bool s_last;
   const int tid = threadIdx.x;
   const int run = tid / kJoinCols, c = tid % kJoinCols;
   double part = 0.0;
@@ -329,18 +334,39 @@ __global__ __launch_bounds__(kJoinThreads) void k_balance_join(BalanceArgs a, in
     }
     __syncthreads();
   }
-  if (tid >= kJoinCols) return;
+  if (tid < kJoinCols) {
 #pragma unroll
-  for (int off = 1; off < kJoinCols; off <<= 1) part += __shfl_xor(part, off, kJoinCols);
+    for (int off = 1; off < kJoinCols; off <<= 1) part += __shfl_xor(part, off, kJoinCols);
+  }
+  uint32_t* const high = reinterpret_cast<uint32_t*>(a.part_sum);
+  uint32_t* const low = reinterpret_cast<uint32_t*>(a.part_count);
+  if (tid == 0) {
+    const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(part));
+    const int64_t at = part_at(a, chunk, cols, blockIdx.x);
+    const uint32_t h = __hip_atomic_exchange(high + at, static_cast<uint32_t>(bits >> 32), __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t l =
+        __hip_atomic_exchange(low + at, static_cast<uint32_t>(bits), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" : : "v"(h), "v"(l) : "memory");  // both have returned
+    s_last = __hip_atomic_fetch_add(a.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  part = 0.0;
+  for (int i = tid; i < static_cast<int>(gridDim.x); i += kJoinThreads) {
+    const int64_t at = part_at(a, chunk, cols, i);
+    // (exchanges, since a load might find an older line in this XCD's L2)
+    const uint64_t h = __hip_atomic_exchange(high + at, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint64_t l = __hip_atomic_exchange(low + at, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    part += __longlong_as_double(static_cast<long long>(h << 32 | l));
+  }
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) part += __shfl_xor(part, off, kWave);
+  if ((tid & (kWave - 1)) == 0) s_part[tid / kWave] = part;
+  __syncthreads();
   if (tid != 0) return;
-  // offsets out of order may give anything
-  part = fmin(fmax(part * a.E / (static_cast<double>(a.K) * a.B), 0.0), static_cast<double>(a.E));
-  const unsigned long long mine =
-      static_cast<unsigned long long>(part * (1ull << kFraction) + 0.5) + (1ull << kCountShift);
-  const unsigned long long before = __hip_atomic_fetch_add(a.total, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if ((before >> kCountShift) != gridDim.x - 1) return;
-  const unsigned long long all = (before + mine) & ((1ull << kCountShift) - 1);
-  a.loss[0] = static_cast<float>(static_cast<double>(all) / (1ull << kFraction) * a.coef);
+  for (int w = 1; w < kJoinThreads / kWave; ++w) part += s_part[w];
+  a.loss[0] = static_cast<float>(part * a.E / (static_cast<double>(a.K) * a.B) * a.coef);
 }
 
 // no token: every output is 0

@@ -78,7 +78,7 @@ struct BalanceGeom {
   int64_t slots;   // chunks + B
   int cols;        // column groups of the join, ceil(E / 16)
   int joins;       // blocks of the join
-  // workspace parts, multiples of 16, and the word that the join's blocks add to
+  // workspace parts, multiples of 16, and the word that counts the join's finished blocks
   size_t sum_bytes, count_bytes, token_bytes;
   size_t bytes() const { return sum_bytes + count_bytes + token_bytes + 16; }
 };
@@ -102,11 +102,11 @@ struct BalanceArgs {
   float scale;  // coef * E / (K * B)
   float coef;
   // workspace: by slot, sums [slots, E], counts [slots, E], tokens [slots]; the
-  // join's word
+  // join's finished blocks
   float* part_sum;
   int32_t* part_count;
   int32_t* part_tokens;
-  unsigned long long* total;
+  unsigned* done;
 };
 hipError_t launch_balance(const BalanceArgs& a, const BalanceGeom& g, hipStream_t s);
 hipError_t launch_balance_backward(const BalanceArgs& a, hipStream_t s);

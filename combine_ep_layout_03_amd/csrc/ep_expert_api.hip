@@ -264,7 +264,7 @@ int ep_balance_loss(const ep_balance_t* b, const void* logits, const int64_t* to
     a.part_sum = reinterpret_cast<float*>(part(g.sum_bytes));
     a.part_count = reinterpret_cast<int32_t*>(part(g.count_bytes));
     a.part_tokens = reinterpret_cast<int32_t*>(part(g.token_bytes));
-    a.total = reinterpret_cast<unsigned long long*>(ws);
+    a.done = reinterpret_cast<unsigned*>(ws);
   }
   return ep::launch_balance(a, g, stream) == hipSuccess ? EP_OK : EP_EHIP;
 }
