@@ -73,11 +73,15 @@ inline bool workspace_overlaps(const void* workspace, size_t bytes, std::initial
   return false;
 }
 
+// Rows of the receive buffers at most, the padding of aligned segments included.
 inline int64_t max_rows(const ep_problem_t* p) {
   const int64_t pad = static_cast<int64_t>(p->num_experts) *
                       (p->expert_alignment > 1 ? p->expert_alignment - 1 : 0);
   return p->num_tokens * p->topk + pad;
 }
+
+// Rows of a selection at most: what the experts' counts add up to.
+inline int64_t selections(const ep_problem_t* p) { return p->num_tokens * p->topk; }
 
 // A matrix of rows: stride (0 = width), alignment.
 inline int check_rows(const void* p, int64_t stride, int32_t width, int64_t* ld) {

@@ -64,9 +64,11 @@ struct ActBackwardArgs {
   uint32_t generation;
 };
 
+// rows: of a selection, at most
 hipError_t launch_linear(const LinearArgs& a, int64_t rows, hipStream_t s);
 // grad_x of x and grad_w of w, either null
 hipError_t launch_linear_grads(const LinearArgs* x, const LinearArgs* w, int64_t rows, hipStream_t s);
+// rows: up to offsets[E], at most
 hipError_t launch_act_backward(const ActBackwardArgs& a, int64_t rows, hipStream_t s);
 
 // The balance loss.  Tokens are taken in chunks of a fixed size; the part of

@@ -36,8 +36,8 @@ int check_linear(const ep_problem_t* p, const ep_linear_t* lin) {
   const int64_t W = lin->gated ? 2LL * lin->n_out : lin->n_out;
   if (p->hidden > kMaxWidth || W > kMaxWidth || W * p->hidden > INT32_MAX) return EP_ENOTSUP;
   // fewer than 2^32 threads in 512 a block, the rounds that a launch is filled up to included
-  return ep::linear_max_tiles(max_rows(p), p->num_experts, p->hidden, static_cast<int>(W)) < (1 << 22) ? EP_OK
-                                                                                                    : EP_ENOTSUP;
+  const int64_t tiles = ep::linear_max_tiles(selections(p), p->num_experts, p->hidden, static_cast<int>(W));
+  return tiles < (1 << 22) ? EP_OK : EP_ENOTSUP;
 }
 
 int check_stride(const void* p, int64_t stride, int32_t width, int64_t* ld) {
@@ -129,12 +129,12 @@ int ep_expert_linear(const ep_problem_t* p, const ep_layout_t* L, const ep_linea
   a.res = static_cast<const uint16_t*>(residual);
   a.out = static_cast<uint16_t*>(out);
   a.pre = static_cast<uint16_t*>(pre);
-  return ep::launch_linear(a, rows, stream) == hipSuccess ? EP_OK : EP_EHIP;
+  return ep::launch_linear(a, selections(p), stream) == hipSuccess ? EP_OK : EP_EHIP;
 }
 
 size_t ep_expert_linear_workspace_bytes(const ep_problem_t* p, const ep_linear_t* lin) {
   if (check_linear(p, lin) != EP_OK) return 0;
-  return ep::linear_geom(max_rows(p), p->num_experts, p->hidden, width_of(lin)).part_bytes;
+  return ep::linear_geom(selections(p), p->num_experts, p->hidden, width_of(lin)).part_bytes;
 }
 
 int ep_expert_linear_backward(const ep_problem_t* p, const ep_layout_t* L, const ep_linear_t* lin,
@@ -169,7 +169,7 @@ int ep_expert_linear_backward(const ep_problem_t* p, const ep_layout_t* L, const
   }
   if (a.xmap && grad_w && p->num_tokens * a.ldx * 2 > kMaxGather) return EP_ENOTSUP;
   const int64_t rows = max_rows(p);
-  const ep::LinearGeom g = ep::linear_geom(rows, a.E, a.H, a.W);
+  const ep::LinearGeom g = ep::linear_geom(selections(p), a.E, a.H, a.W);
   const int64_t nw = 2LL * a.E * a.W * a.H, nb = 2LL * a.E * a.W;
   const Rows ro = {grad_out, rows, 2LL * a.N, 2 * ldgo};
   const Rows rx = {grad_w ? x : nullptr, a.xmap ? p->num_tokens : rows, 2LL * a.H, 2 * a.ldx};
@@ -211,7 +211,7 @@ int ep_expert_linear_backward(const ep_problem_t* p, const ep_layout_t* L, const
   ax.out = static_cast<uint16_t*>(grad_x);
   a.splits = g.splits;
   a.part = static_cast<float*>(workspace);
-  return ep::launch_linear_grads(grad_x ? &ax : nullptr, grad_w ? &a : nullptr, rows, stream) == hipSuccess
+  return ep::launch_linear_grads(grad_x ? &ax : nullptr, grad_w ? &a : nullptr, selections(p), stream) == hipSuccess
              ? EP_OK
              : EP_EHIP;
 }

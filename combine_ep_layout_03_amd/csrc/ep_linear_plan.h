@@ -1,4 +1,6 @@
 // How the products of an expert's layer are launched, from the sizes alone.
+// `rows` is what the experts' counts add up to at most: rows of padding between
+// aligned segments are in no tile.
 // Host code without HIP, so that it can be run and tested anywhere.
 #pragma once
 

@@ -59,9 +59,10 @@ typedef struct ep_linear {
  * gathered x, T * K + E * (A - 1) otherwise, A the alignment or 1).
  * Requires H % 8 == 0, N % 8 == 0, row strides multiples of 8 up to 2^21,
  * bases 16-byte aligned, W and H up to 2^20 with W * H < 2^31, fewer than
- * 2^22 tiles of 128 rows x 128 columns and, with gathered rows, x of 64 GiB at
- * most (EP_ENOTSUP for sizes, EP_EINVAL for strides and bases).  Other flags
- * than EP_FLAG_GATHER_ROWS are refused.  A stale L writes nothing but
+ * 2^22 tiles of 128 rows x 128 columns (of the T * K selections; padding counts
+ * in no tile) and, with gathered rows, x of 64 GiB at most (EP_ENOTSUP for
+ * sizes, EP_EINVAL for strides and bases).  Other flags than
+ * EP_FLAG_GATHER_ROWS are refused.  A stale L writes nothing but
  * EP_STATUS_STALE = 1. */
 int ep_expert_linear(const ep_problem_t* p, const ep_layout_t* L, const ep_linear_t* lin,
                      const void* x, int64_t x_row_stride, const void* residual,
