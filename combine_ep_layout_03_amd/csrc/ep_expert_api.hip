@@ -182,9 +182,11 @@ int ep_expert_linear_backward(const ep_problem_t* p, const ep_layout_t* L, const
       any_overlap(gw, {ro, rx, rw, rp, gb}) || any_overlap(gb, {ro, rx, rw, rp}))
     return EP_EINVAL;
   if (!(pre == grad_pre && b.ldpre == b.ldgpre) && any_overlap(gp, {rp})) return EP_EINVAL;
-  if (!workspace || !aligned(workspace, 16)) return EP_EINVAL;
-  if (workspace_bytes < g.part_bytes) return EP_EWORKSPACE;
-  if (workspace_overlaps(workspace, g.part_bytes, {ro, rx, rw, rp, gp, gx, gw, gb})) return EP_EINVAL;
+  if (grad_w) {  // nothing else uses it
+    if (!workspace || !aligned(workspace, 16)) return EP_EINVAL;
+    if (workspace_bytes < g.part_bytes) return EP_EWORKSPACE;
+    if (workspace_overlaps(workspace, g.part_bytes, {ro, rx, rw, rp, gp, gx, gw, gb})) return EP_EINVAL;
+  }
   a.x = static_cast<const uint16_t*>(x);
   if (bare) {
     a.g = static_cast<const uint16_t*>(grad_out);

@@ -139,8 +139,8 @@ def ep_expert_linear_backward(
     not; the bias's comes with the weights').  An expert without rows gets zero
     weight gradients; rows of no selection are not written.  The gradient of
     the residual is grad_out itself.  ``workspace`` (uint8,
-    ``ep_expert_linear_workspace_bytes``) is allocated if not given; calls that
-    may overlap need their own."""
+    ``ep_expert_linear_workspace_bytes``) is for the weights' and allocated if
+    not given; calls that may overlap need their own."""
     layout, gen = _resolve(layout)
     W, N, H, rows, xrows, index, shape, p, s, lin = _linear_args(layout, gen, w, None, activation, gated, gather)
     _rows(grad_out, "grad_out", N, rows, index)
@@ -178,14 +178,14 @@ def ep_expert_linear_backward(
             grad_bias = w.new_empty((w.shape[0], W))
         else:
             _check(grad_bias, "grad_bias", _BF16, (w.shape[0], W), index)
-    if workspace is None:
-        workspace = w.new_empty(_linear_workspace(*shape, N, int(activation), int(bool(gated))), dtype=_U8)
-    else:
+    if workspace is not None:
         _check(workspace, "workspace", _U8, None, index)
+    elif need_w:
+        workspace = w.new_empty(_linear_workspace(*shape, N, int(activation), int(bool(gated))), dtype=_U8)
     _call("ep_expert_linear_backward", index, p, s, lin, grad_out.data_ptr(), grad_out.shape[1],
           x.data_ptr() if need_w else None, x.shape[1] if need_w else 0, _ptr(pre), _stride(pre), _ptr(grad_pre),
-          _stride(grad_pre), _ptr(grad_x), _stride(grad_x), _ptr(grad_w), _ptr(grad_bias), workspace.data_ptr(),
-          workspace.numel())
+          _stride(grad_pre), _ptr(grad_x), _stride(grad_x), _ptr(grad_w), _ptr(grad_bias), _ptr(workspace),
+          0 if workspace is None else workspace.numel())
     return grad_x, grad_w, grad_bias, grad_pre
 
 

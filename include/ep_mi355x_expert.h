@@ -100,7 +100,8 @@ size_t ep_expert_linear_workspace_bytes(const ep_problem_t* p, const ep_linear_t
  * Limits as in ep_expert_linear; the outputs must overlap neither an input nor
  * each other.  `workspace` of ep_expert_linear_workspace_bytes, 16-byte
  * aligned (its contents need no initialisation and are clobbered; calls that
- * may overlap in time need their own). */
+ * may overlap in time need their own); not used, and may be NULL, without
+ * grad_w. */
 int ep_expert_linear_backward(const ep_problem_t* p, const ep_layout_t* L, const ep_linear_t* lin,
                               const void* grad_out, int64_t grad_out_row_stride, const void* x,
                               int64_t x_row_stride, const void* pre, int64_t pre_row_stride,

@@ -156,3 +156,32 @@ def test_last_rows_past_32_bits_within_the_bound(device):
         y = m.ep_expert_linear(x, L, w, gather=gather)
         assert (np.abs(base.f64(y[-50:]) - want) <= bound).all()
         assert not y[:-50].any()
+
+
+@gpu
+def test_grad_x_alone_takes_no_workspace(device):
+    """Rows enough that the weight gradient would be split: grad_x alone
+    allocates itself and no parts, and is the same."""
+    m = base.ep()
+    T, H, N = 16384, 1024, 1024
+    L = m.ep_layout(torch.zeros(T, 1, dtype=torch.int64, device=DEV), 1)
+    parts = m.ep_expert_linear_workspace_bytes(L, H, N)
+    assert parts > 16 << 20
+    g = torch.Generator().manual_seed(3)
+    x, go, w = base.bf(g, 1.0, T, H).to(DEV), base.bf(g, 1.0, T, N).to(DEV), base.bf(g, 0.1, 1, N, H).to(DEV)
+    want = m.ep_expert_linear_backward(go, x, L, w)[0]
+    got = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    m.ep_expert_linear_backward(go, x, L, w, grad_x=got, needs=(True, False))
+    torch.cuda.synchronize()
+    assert torch.cuda.max_memory_allocated() - before < 1 << 20
+    assert torch.equal(got, want)
+    # one that is too small for the parts is no matter either
+    got.zero_()
+    small = torch.empty(16, dtype=torch.uint8, device=DEV)
+    m.ep_expert_linear_backward(go, x, L, w, grad_x=got, needs=(True, False), workspace=small)
+    assert torch.equal(got, want)
+    with pytest.raises(m.EPError):
+        m.ep_expert_linear_backward(go, x, L, w, needs=(False, True), workspace=small)
