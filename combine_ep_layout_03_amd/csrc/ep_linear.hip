@@ -66,23 +66,34 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // a pointer that is the same in every lane, as the compiler may not know
 __device__ __forceinline__ const char* scalar(const char* p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(v));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<int>(v >> 32));
+  uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(v));
+  uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<int>(v >> 32));
+  // a scalar register that a vector instruction wrote may be a load's address 5
+  // wait states later, which the compiler does not count for the loads below
+  asm volatile("s_nop 4" : "+s"(lo), "+s"(hi));
   return reinterpret_cast<const char*>((static_cast<uint64_t>(hi) << 32) | lo);
 }
 
 // 16 bytes a lane from base + off to LDS at `to` + 16 lane, not tracked by the
 // compiler: its wait counts cannot tell the stages of a ring apart, and would
 // drain every load before each LDS read.  wait_vm below is what waits.
+// m0 is named as clobbered, so that no value of the compiler's is kept there
+// (it warns that the register is one of its own, which it is).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_lds16(const char* base, uint32_t off, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
                : "s"(to), "v"(off), "s"(base)
-               : "memory");
+               : "m0", "memory");
 }
 __device__ __forceinline__ void load_lds16(const char* p, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(to), "v"(p) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(to), "v"(p)
+               : "m0", "memory");
 }
+#pragma clang diagnostic pop
 
 // wait until at most n vector-memory loads of this wave are outstanding
 // (rounded down to a value listed); the other counters are left alone
