@@ -6,16 +6,16 @@
 //     grad_logits[t, e] = p_e (f_e - sum_j f_j p_j) (* 1 - s_e for sigmoid),
 //     f_e = grad_loss coef E c[e] / (B K n^2).
 //
-// Bound by memory: the logits are read once (65,536 x 256 fp32: 67 MB; forward
-// 20 us and 8 us of the join, the gradient with a base 45 us for 201 MB, 47
-// without loading a row ahead), and the gradient writes as many.  A token has
-// 16 lanes (64 above 256 experts), so a wave works on four tokens at once and a token's maximum and sum cost
-// four lane moves within a row of 16.  A lane keeps the same experts for
-// every token of its block, so the sums over tokens stay in registers until
-// the block's tokens of a sequence are through, and the gradient's f does.
-// Sums go block by block into slots of the workspace and a second kernel adds
-// the slots in their order: no floating-point atomics, equal inputs give
-// equal bytes.
+// The logits are read once (65,536 x 256 fp32: 67 MB).  Forward 20 us, bound by
+// the latency of each element's exponential and quotient, and 10 us of the join;
+// the gradient with a base is bound by memory, 45 us for 201 MB (47 without
+// loading a row ahead).  A token has 16 lanes (64 above 256 experts), so a wave
+// works on four tokens at once and a token's maximum and sum cost four lane
+// moves within a row of 16.  A lane keeps the same experts for every token of
+// its block, so the sums over tokens stay in registers until the block's tokens
+// of a sequence are through, and the gradient's f does.  Sums go block by block
+// into slots of the workspace and a second kernel adds the slots in their order:
+// no floating-point atomics, equal inputs give equal bytes.
 #include <float.h>
 
 #include "ep_expert.h"

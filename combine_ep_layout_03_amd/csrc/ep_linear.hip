@@ -126,13 +126,15 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhScale = 0.79788456080286536f;  // sqrt(2 / pi)
 constexpr float kTanhCubic = 0.044715f;
 
-// The normal distribution function, erfc(-z / sqrt 2) / 2, to a few steps of
-// fp32 also where it is tiny.  (1 + 2 x) exp(x^2) erfc(x) is smooth over all x
-// >= 0 in s = (x - k) / (x + k) (Shepherd and Laframboise, Math. Comp. 36,
-// 1981); the coefficients are a Chebyshev fit of degree 9 for k = 2.5 up to x =
-// 12, where exp(-x^2) is below fp32 (relative error 2.6e-8, 1.5e-7 in fp32).  A
-// few dozen instructions without a branch; erfcf's two branches took 1262
-// spilled registers with 8 elements a lane.
+// The normal distribution function, erfc(-z / sqrt 2) / 2.  (1 + 2 x) exp(x^2)
+// erfc(x) is smooth over all x >= 0 in s = (x - k) / (x + k) (Shepherd and
+// Laframboise, Math. Comp. 36, 1981); the coefficients are a Chebyshev fit of
+// degree 9 for k = 2.5 up to x = 12, where exp(-x^2) is below fp32 (relative
+// error 6.5e-8).  In fp32 the result's relative error is 4e-7 down to z = -2
+// and grows with the rounding of the exponential's argument to 8e-6 at -13, far
+// below the bf16 half step of 3.9e-3 that the results end in.  A few dozen
+// instructions without a branch; erfcf's two branches took 1262 spilled
+// registers with 8 elements a lane.
 __device__ __forceinline__ float normal_cdf(float z) {
   constexpr float kFit[10] = {1.26483822f, -0.122356892f, -0.0990232155f, 0.15763326f, -0.102984153f, 0.0327342302f, 0.00100810081f, -0.0042856955f, 0.000354380376f, 0.000468412938f};
   const float x = fminf(fabsf(z) * kSqrtHalf, 12.0f);
@@ -1002,7 +1004,12 @@ __global__ __launch_bounds__(kBlock) void k_linear_join(const float* part, int s
   *reinterpret_cast<u32x4*>(weights ? gw + at : gb + (at - nw)) = b;
 }
 
-// 8 columns a lane; a wave walks the columns of one row.
+// 8 columns a lane; a wave walks the columns of one row.  grad_pre is rounded to
+// bf16 here, before the products that are formed from it: the matrix
+// instructions take bf16, and the gradients are of the grad_pre that is
+// returned.  It adds its error to that of the results' own rounding (2.4e-3 of
+// their norm against 1.7e-3); keeping it as two bf16 parts would take each
+// product twice.
 __global__ __launch_bounds__(kBlock) void k_act_backward(ActBackwardArgs a) {
   if (!layout_current(a.status, a.generation)) return;
   const int lane = lane_id();
